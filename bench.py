@@ -50,7 +50,7 @@ def _profiled_traffic(key: str):
     if key not in PROFILE_KEYS:
         return None
     prof = os.path.join(ROOT, "profiles", f"split_kernel_{PROFILE_KEYS[key]}.txt")
-    src = os.path.join(ROOT, "packed_cache_decode_b200", "csrc", "decode_mma.cu")
+    src = os.path.join(ROOT, "packed_cache_decode_b200", "csrc", "decode_split.cuh")
     try:
         fields = dict(ln.split(":", 1) for ln in open(prof) if ln.startswith(("source_sha256_16:", "dram_bytes")))
         with open(src, "rb") as f:

@@ -85,6 +85,7 @@ enum { BGTQ_F32 = 0, BGTQ_BF16 = 1, BGTQ_F16 = 2 };
 #define BGTQ_TILE_TOKENS 64
 #define BGTQ_MAX_GQA 32  /* query columns per KV head: (h_q / h_kv) x query tokens */
 #define BGTQ_MAX_KGROUPS 4
+#define BGTQ_MAX_TREE 64 /* drafted tokens per row of a tree call (bits of a mask word) */
 
 /* Device status bits reported by bgtq_device_status. */
 #define BGTQ_STATUS_ENCODE_OVERFLOW 1u  /* encode: seq_len + n_new > capacity; those tokens skipped */
@@ -93,6 +94,8 @@ enum { BGTQ_F32 = 0, BGTQ_BF16 = 1, BGTQ_F16 = 2 };
                                            wait; that call's output is invalid */
 #define BGTQ_STATUS_BAD_PAGE 8u        /* paged calls: a block-table entry outside the pool; the encode
                                           skips that token, the attention reads nothing for that tile */
+#define BGTQ_STATUS_BAD_TREE 16u       /* tree calls: a row's node count, path or length does not fit the call;
+                                          the attention writes zeros for that row, the commit leaves it alone */
 
 typedef struct bgtq_layout bgtq_layout;
 
@@ -421,6 +424,124 @@ bgtq_status bgtq_decode_step_paged_heads(const bgtq_layout_set* set, const void*
                                          size_t workspace_bytes, void* stream);
 /* The set's status bits (BGTQ_STATUS_*), as bgtq_device_status. */
 bgtq_status bgtq_layout_set_status(const bgtq_layout_set* set, unsigned* flags, int clear);
+
+/* ---------------------------------------------------------------- drafted trees */
+
+/* The three groups of calls below serve a packed cache in ways the pages do not describe
+ * (drafted trees, a bound on the cache); they read, and move bit for bit, the same format. */
+
+/* Workspace bytes of bgtq_tree_attention (and its paged form) for this shape on the current
+ * device. 0 on bad arguments. */
+size_t bgtq_tree_workspace_bytes(const bgtq_layout* layout, int batch, int h_q, int h_kv, int n_q,
+                                 long long max_seq_len);
+/* Attention of a tree of drafted tokens over the packed cache (speculative verification).
+ * The tree's n nodes are the last n cached tokens of their row (appended before, e.g. by
+ * bgtq_encode_append, keys rotated for their depth): node j sits at cache position
+ * seq_len - n + j. Its query sees every token before the nodes, and node i when bit i of
+ * tree_mask_dev[b * n_q + j] is set (set the node's own bit to let it see itself; bits at
+ * or past n are ignored). n = n_nodes_dev[b], or n_q for every row when n_nodes_dev is
+ * null; 1 <= n_q <= BGTQ_MAX_TREE. q [batch, n_q, h_q, 128] (q_dtype), out [batch, n_q,
+ * h_q, 128] of out_dtype (fp32, bf16 or fp16): rows j >= n are not written; a query that
+ * sees no token gives zeros. A row with n outside 0..n_q or above its length is flagged
+ * (BGTQ_STATUS_BAD_TREE) and gets zeros. A length past max_seq_len or the capacity is
+ * clamped and flagged; the nodes are then the last n tokens of the clamped row. The mask,
+ * the lengths and the node counts are device memory; a mask of a causal run (bits 0..j of
+ * node j) gives bgtq_decode_attention_multi's result. Accuracy as bgtq_decode_attention.
+ * Other arguments, ownership and errors as bgtq_decode_attention; the cache must be
+ * 16-byte aligned. */
+bgtq_status bgtq_tree_attention(const bgtq_layout* layout, const void* q, int q_dtype, int batch, int n_q,
+                                int h_q, int h_kv, const unsigned long long* tree_mask_dev,
+                                const int* n_nodes_dev, const void* cache, const int* seq_lens_dev,
+                                long long capacity, long long max_seq_len, float softmax_scale, void* out,
+                                int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+/* bgtq_tree_attention over a paged cache (pool, num_pages and block table as
+ * bgtq_decode_attention_paged). */
+bgtq_status bgtq_tree_attention_paged(const bgtq_layout* layout, const void* q, int q_dtype, int batch,
+                                      int n_q, int h_q, int h_kv, const unsigned long long* tree_mask_dev,
+                                      const int* n_nodes_dev, const void* pool, long long num_pages,
+                                      const int* block_table_dev, long long max_pages,
+                                      const int* seq_lens_dev, long long max_seq_len, float softmax_scale,
+                                      void* out, int out_dtype, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+/* Keeps the accepted path of each row's tree: cached token seq_len - n + path[i] becomes
+ * token seq_len - n + i for i = 0 .. n_path - 1, in every KV head, codes and norms bit for
+ * bit; the new length is seq_len - n + n_path (tokens at or past it are dropped: the next
+ * append overwrites them; tokens from there to seq_len keep their bytes). path_dev
+ * [batch, path_ld] (path_ld >= n_q), n_path_dev[batch], n as in bgtq_tree_attention
+ * (n_nodes_dev or n_q); new_lens_dev[batch] receives the lengths and must not overlap
+ * seq_lens_dev. A path may name nodes in any order, or one twice. A row whose n, n_path,
+ * path or length does not fit (n_path > n, a node outside 0..n-1, n > seq_len, seq_len >
+ * capacity) is flagged (BGTQ_STATUS_BAD_TREE) and keeps its tokens and its length. */
+bgtq_status bgtq_tree_commit(const bgtq_layout* layout, const int* path_dev, int path_ld,
+                             const int* n_path_dev, const int* n_nodes_dev, int n_q, int batch, int h_kv,
+                             void* cache, const int* seq_lens_dev, int* new_lens_dev, long long capacity,
+                             void* stream);
+/* The same on a paged cache (a row with a page outside the pool among its nodes' tiles is
+ * flagged BGTQ_STATUS_BAD_PAGE and keeps its tokens; its new length is written). */
+bgtq_status bgtq_tree_commit_paged(const bgtq_layout* layout, const int* path_dev, int path_ld,
+                                   const int* n_path_dev, const int* n_nodes_dev, int n_q, int batch,
+                                   int h_kv, void* pool, long long num_pages, const int* block_table_dev,
+                                   long long max_pages, const int* seq_lens_dev, int* new_lens_dev,
+                                   void* stream);
+
+/* ---------------------------------------------------------------- a bounded cache */
+
+/* Workspace bytes of bgtq_decode_attention_mass (and its paged form) for this shape on the
+ * current device: bgtq_workspace_bytes plus 4 bytes per query head and token of max_seq_len
+ * (rounded up to whole tiles). 0 on bad arguments. */
+size_t bgtq_mass_workspace_bytes(const bgtq_layout* layout, int batch, int h_q, int h_kv,
+                                 long long max_seq_len);
+/* bgtq_decode_attention that also keeps the attention mass of every cached token:
+ *   mass[(b * h_kv + h) * mass_ld + t] = decay * itself + sum of the softmax weights of
+ *   token t over the query heads of KV head h,  t < seq_len
+ * (fp32 device, owned by the caller, zeroed before a token's first step; entries at or past
+ * the length are not touched; mass_ld >= max_seq_len). decay = 1 gives the plain sum; it
+ * must be finite. out [batch, h_q, 128] of out_dtype (fp32, bf16 or fp16). With a length of
+ * 0 the output row is zero. Two calls at once need a workspace each. Other arguments,
+ * ownership and errors as bgtq_decode_attention. */
+bgtq_status bgtq_decode_attention_mass(const bgtq_layout* layout, const void* q, int q_dtype, int batch,
+                                       int h_q, int h_kv, const void* cache, const int* seq_lens_dev,
+                                       long long capacity, long long max_seq_len, float softmax_scale,
+                                       float decay, float* mass, long long mass_ld, void* out, int out_dtype,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+/* The same over a paged cache (a tile without a page in the pool is left out: its tokens
+ * get no weight). */
+bgtq_status bgtq_decode_attention_mass_paged(const bgtq_layout* layout, const void* q, int q_dtype, int batch,
+                                             int h_q, int h_kv, const void* pool, long long num_pages,
+                                             const int* block_table_dev, long long max_pages,
+                                             const int* seq_lens_dev, long long max_seq_len,
+                                             float softmax_scale, float decay, float* mass, long long mass_ld,
+                                             void* out, int out_dtype, void* workspace,
+                                             size_t workspace_bytes, void* stream);
+/* Eviction: copies the tokens worth keeping of every (row, KV head) into another cache.
+ * A row of at most `keep` tokens keeps all of them; else the first n_sink, the last
+ * n_recent, and of the others the keep - n_sink - n_recent with the largest mass (equal
+ * mass: the lowest position; NaN below everything), each KV head its own. They stay in
+ * their order, codes and norms bit for bit (keys stay rotated for their old positions).
+ * src [batch][h_kv][src_capacity / 64] tiles, dst likewise with dst_capacity >= the tokens
+ * kept; the rest of a row's last tile is zeroed, later tiles are not touched. mass
+ * [batch, h_kv, mass_ld >= max_seq_len]; mass_out [batch, h_kv, mass_out_ld] receives the
+ * kept tokens' mass, then zeros up to mass_out_ld; kept_dev [batch, h_kv, keep] int32 their
+ * old positions, then -1; new_lens_dev[batch] = min(seq_len, keep). Needs keep >= 1,
+ * n_sink, n_recent >= 0, n_sink + n_recent <= keep; lengths past max_seq_len are clamped
+ * and flagged. No buffer that is written may overlap one that is read (checked for the
+ * caches, the masses and the lengths); caches must be 16-byte aligned. */
+bgtq_status bgtq_cache_evict(const bgtq_layout* layout, int batch, int h_kv, const void* src,
+                             long long src_capacity, const int* seq_lens_dev, long long max_seq_len,
+                             const float* mass, long long mass_ld, int keep, int n_sink, int n_recent,
+                             void* dst, long long dst_capacity, float* mass_out, long long mass_out_ld,
+                             int* kept_dev, int* new_lens_dev, void* stream);
+/* The same between paged caches, which may share one pool: the pages that dst_table names
+ * for the kept tokens must not be among the row's own or another row's source pages. A
+ * source tile without a page in the pool gives zero codes and norms, a destination tile
+ * without one is left out; both are flagged (BGTQ_STATUS_BAD_PAGE). */
+bgtq_status bgtq_cache_evict_paged(const bgtq_layout* layout, int batch, int h_kv, const void* src_pool,
+                                   long long src_pages, const int* src_table_dev, long long src_max_pages,
+                                   const int* seq_lens_dev, long long max_seq_len, const float* mass,
+                                   long long mass_ld, int keep, int n_sink, int n_recent, void* dst_pool,
+                                   long long dst_pages, const int* dst_table_dev, long long dst_max_pages,
+                                   float* mass_out, long long mass_out_ld, int* kept_dev, int* new_lens_dev,
+                                   void* stream);
 
 /* ---------------------------------------------------------------- no-allocation variant */
 

@@ -21,6 +21,8 @@ STATUS_ENCODE_OVERFLOW = 1
 STATUS_DECODE_CLAMPED = 2
 STATUS_TIMEOUT = 4
 STATUS_BAD_PAGE = 8
+STATUS_BAD_TREE = 16
+MAX_TREE = 64
 LAYOUT_NORM_CORRECT = 1
 LAYOUT_NORM_FP16 = 2
 
@@ -38,6 +40,9 @@ EXPORTED = [
     "bgtq_decode_step_heads", "bgtq_layout_set_paged_pool_bytes", "bgtq_encode_append_paged_heads",
     "bgtq_decode_attention_paged_heads", "bgtq_decode_attention_multi_heads", "bgtq_decode_step_multi_heads",
     "bgtq_decode_step_paged_heads",
+    "bgtq_tree_workspace_bytes", "bgtq_tree_attention", "bgtq_tree_attention_paged", "bgtq_tree_commit",
+    "bgtq_tree_commit_paged", "bgtq_mass_workspace_bytes", "bgtq_decode_attention_mass",
+    "bgtq_decode_attention_mass_paged", "bgtq_cache_evict", "bgtq_cache_evict_paged",
 ]
 
 
@@ -112,6 +117,17 @@ def load():
         "bgtq_decode_step_multi_heads": (I, [P, P, P, I, I, P, I, I, I, P, P, LL, LL, F, P, P, C.c_size_t, P]),
         "bgtq_decode_step_paged_heads": (I, [P, P, P, I, I, P, I, I, I, P, LL, P, LL, P, LL, F, P, P, C.c_size_t,
                                              P]),
+        "bgtq_tree_workspace_bytes": (C.c_size_t, [P, I, I, I, I, LL]),
+        "bgtq_tree_attention": (I, [P, P, I, I, I, I, I, P, P, P, P, LL, LL, F, P, I, P, C.c_size_t, P]),
+        "bgtq_tree_attention_paged": (I, [P, P, I, I, I, I, I, P, P, P, LL, P, LL, P, LL, F, P, I, P, C.c_size_t, P]),
+        "bgtq_tree_commit": (I, [P, P, I, P, P, I, I, I, P, P, P, LL, P]),
+        "bgtq_tree_commit_paged": (I, [P, P, I, P, P, I, I, I, P, LL, P, LL, P, P, P]),
+        "bgtq_mass_workspace_bytes": (C.c_size_t, [P, I, I, I, LL]),
+        "bgtq_decode_attention_mass": (I, [P, P, I, I, I, I, P, P, LL, LL, F, F, P, LL, P, I, P, C.c_size_t, P]),
+        "bgtq_decode_attention_mass_paged": (I, [P, P, I, I, I, I, P, LL, P, LL, P, LL, F, F, P, LL, P, I, P,
+                                                 C.c_size_t, P]),
+        "bgtq_cache_evict": (I, [P, I, I, P, LL, P, LL, P, LL, I, I, I, P, LL, P, LL, P, P, P]),
+        "bgtq_cache_evict_paged": (I, [P, I, I, P, LL, P, LL, P, LL, P, LL, I, I, I, P, LL, P, LL, P, LL, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -688,3 +704,175 @@ def decode_step_paged_heads(layouts: LayoutSet, k_new, v_new, q, pc, seq_lens, m
                                                C.c_void_p(out.data_ptr()), C.c_void_p(workspace.data_ptr()),
                                                workspace.numel(), _stream_ptr(stream)),
            "decode_step_paged_heads")
+
+
+# ---------------------------------------------------------------- drafted trees
+def tree_workspace_bytes(layout: Layout, batch: int, h_q: int, h_kv: int, n_q: int, max_seq_len: int) -> int:
+    n = load().bgtq_tree_workspace_bytes(layout.handle, batch, h_q, h_kv, n_q, max_seq_len)
+    if n == 0:
+        _check(ERR_INVALID, "tree_workspace_bytes")
+    return int(n)
+
+
+def _opt(t):
+    return C.c_void_p(None if t is None else t.data_ptr())
+
+
+def _tree_shapes(q, tree_mask, n_nodes, seq_lens, out):
+    import torch
+    B_, n_q, h_q, d = q.shape
+    assert d == HEAD_DIM and q.is_contiguous() and out.is_contiguous() and out.shape == q.shape
+    assert tree_mask.dtype in (torch.int64, torch.uint64) and tuple(tree_mask.shape) == (B_, n_q)
+    assert tree_mask.is_contiguous() and seq_lens.dtype == torch.int32 and seq_lens.numel() == B_
+    assert n_nodes is None or (n_nodes.dtype == torch.int32 and n_nodes.numel() == B_)
+    return B_, n_q, h_q
+
+
+def tree_attention(layout: Layout, q, tree_mask, cache, seq_lens, capacity: int, max_seq_len: int, out, workspace,
+                   h_kv: int, n_nodes=None, softmax_scale: float | None = None, stream=None):
+    """Attention of a drafted tree per row over the packed cache that holds its nodes as the
+    row's last tokens: q [B, n_q, h_q, 128] CUDA; tree_mask [B, n_q] int64 CUDA, bit i of
+    word j set when node j sees node i; n_nodes [B] int32 CUDA (None: n_q nodes in every
+    row); out like q (fp32, bf16 or fp16). Rows past a row's nodes are not written."""
+    B_, n_q, h_q = _tree_shapes(q, tree_mask, n_nodes, seq_lens, out)
+    scale = 1.0 / HEAD_DIM ** 0.5 if softmax_scale is None else float(softmax_scale)
+    _check(load().bgtq_tree_attention(layout.handle, C.c_void_p(q.data_ptr()), dtype_code(q), B_, n_q, h_q, h_kv,
+                                      C.c_void_p(tree_mask.data_ptr()), _opt(n_nodes), C.c_void_p(cache.data_ptr()),
+                                      C.c_void_p(seq_lens.data_ptr()), capacity, max_seq_len, scale,
+                                      C.c_void_p(out.data_ptr()), dtype_code(out), C.c_void_p(workspace.data_ptr()),
+                                      workspace.numel(), _stream_ptr(stream)), "tree_attention")
+
+
+def tree_attention_paged(layout: Layout, q, tree_mask, cache: PagedCache, seq_lens, max_seq_len: int, out, workspace,
+                         h_kv: int, n_nodes=None, softmax_scale: float | None = None, stream=None):
+    B_, n_q, h_q = _tree_shapes(q, tree_mask, n_nodes, seq_lens, out)
+    assert cache.table.shape[0] == B_
+    scale = 1.0 / HEAD_DIM ** 0.5 if softmax_scale is None else float(softmax_scale)
+    _check(load().bgtq_tree_attention_paged(layout.handle, C.c_void_p(q.data_ptr()), dtype_code(q), B_, n_q, h_q, h_kv,
+                                            C.c_void_p(tree_mask.data_ptr()), _opt(n_nodes),
+                                            C.c_void_p(cache.pool.data_ptr()), cache.num_pages(layout, h_kv),
+                                            C.c_void_p(cache.table.data_ptr()), cache.max_pages,
+                                            C.c_void_p(seq_lens.data_ptr()), max_seq_len, scale,
+                                            C.c_void_p(out.data_ptr()), dtype_code(out),
+                                            C.c_void_p(workspace.data_ptr()), workspace.numel(), _stream_ptr(stream)),
+           "tree_attention_paged")
+
+
+def _commit_shapes(path, n_path, n_nodes, seq_lens, new_lens):
+    import torch
+    B_, ld = path.shape
+    for t in (path, n_path, seq_lens, new_lens) + (() if n_nodes is None else (n_nodes,)):
+        assert t.dtype == torch.int32 and t.is_contiguous()
+    assert n_path.numel() == B_ and seq_lens.numel() == B_ and new_lens.numel() == B_
+    assert n_nodes is None or n_nodes.numel() == B_
+    return B_, ld
+
+
+def tree_commit(layout: Layout, path, n_path, n_q: int, cache, seq_lens, new_lens, capacity: int, h_kv: int,
+                n_nodes=None, stream=None):
+    """Keeps the accepted nodes path[b, :n_path[b]] of each row's tree (its last n_q, or
+    n_nodes[b], cached tokens) as the tokens after the prefix; new_lens [B] int32 CUDA
+    receives the rows' lengths. path [B, >= n_q], n_path, seq_lens: int32 CUDA."""
+    B_, ld = _commit_shapes(path, n_path, n_nodes, seq_lens, new_lens)
+    _check(load().bgtq_tree_commit(layout.handle, C.c_void_p(path.data_ptr()), ld, C.c_void_p(n_path.data_ptr()),
+                                   _opt(n_nodes), n_q, B_, h_kv, C.c_void_p(cache.data_ptr()),
+                                   C.c_void_p(seq_lens.data_ptr()), C.c_void_p(new_lens.data_ptr()), capacity,
+                                   _stream_ptr(stream)), "tree_commit")
+
+
+def tree_commit_paged(layout: Layout, path, n_path, n_q: int, cache: PagedCache, seq_lens, new_lens, h_kv: int,
+                      n_nodes=None, stream=None):
+    B_, ld = _commit_shapes(path, n_path, n_nodes, seq_lens, new_lens)
+    assert cache.table.shape[0] == B_
+    _check(load().bgtq_tree_commit_paged(layout.handle, C.c_void_p(path.data_ptr()), ld,
+                                         C.c_void_p(n_path.data_ptr()), _opt(n_nodes), n_q, B_, h_kv,
+                                         C.c_void_p(cache.pool.data_ptr()), cache.num_pages(layout, h_kv),
+                                         C.c_void_p(cache.table.data_ptr()), cache.max_pages,
+                                         C.c_void_p(seq_lens.data_ptr()), C.c_void_p(new_lens.data_ptr()),
+                                         _stream_ptr(stream)), "tree_commit_paged")
+
+
+# ---------------------------------------------------------------- a bounded cache
+def mass_workspace_bytes(layout: Layout, batch: int, h_q: int, h_kv: int, max_seq_len: int) -> int:
+    n = load().bgtq_mass_workspace_bytes(layout.handle, batch, h_q, h_kv, max_seq_len)
+    if n == 0:
+        _check(ERR_INVALID, "mass_workspace_bytes")
+    return int(n)
+
+
+def _mass_shapes(q, mass, out, h_kv):
+    import torch
+    B_, h_q, d = q.shape
+    assert d == HEAD_DIM and q.is_contiguous() and out.is_contiguous() and out.shape == q.shape
+    assert mass.dtype == torch.float32 and mass.is_contiguous() and tuple(mass.shape[:2]) == (B_, h_kv)
+    return B_, h_q
+
+
+def decode_attention_mass(layout: Layout, q, cache, seq_lens, capacity: int, max_seq_len: int, mass, out, workspace,
+                          h_kv: int, decay: float = 1.0, softmax_scale: float | None = None, stream=None):
+    """decode_attention that also adds each cached token's attention weight, summed over its
+    KV head's query heads, to decay times mass [B, h_kv, >= max_seq_len] (fp32 CUDA).
+    q [B, h_q, 128]; out like q (fp32, bf16 or fp16)."""
+    B_, h_q = _mass_shapes(q, mass, out, h_kv)
+    scale = 1.0 / HEAD_DIM ** 0.5 if softmax_scale is None else float(softmax_scale)
+    _check(load().bgtq_decode_attention_mass(layout.handle, C.c_void_p(q.data_ptr()), dtype_code(q), B_, h_q, h_kv,
+                                             C.c_void_p(cache.data_ptr()), C.c_void_p(seq_lens.data_ptr()), capacity,
+                                             max_seq_len, scale, decay, C.c_void_p(mass.data_ptr()), mass.shape[2],
+                                             C.c_void_p(out.data_ptr()), dtype_code(out),
+                                             C.c_void_p(workspace.data_ptr()), workspace.numel(),
+                                             _stream_ptr(stream)), "decode_attention_mass")
+
+
+def decode_attention_mass_paged(layout: Layout, q, cache: PagedCache, seq_lens, max_seq_len: int, mass, out,
+                                workspace, h_kv: int, decay: float = 1.0, softmax_scale: float | None = None,
+                                stream=None):
+    B_, h_q = _mass_shapes(q, mass, out, h_kv)
+    assert cache.table.shape[0] == B_
+    scale = 1.0 / HEAD_DIM ** 0.5 if softmax_scale is None else float(softmax_scale)
+    _check(load().bgtq_decode_attention_mass_paged(layout.handle, C.c_void_p(q.data_ptr()), dtype_code(q), B_, h_q,
+                                                   h_kv, C.c_void_p(cache.pool.data_ptr()),
+                                                   cache.num_pages(layout, h_kv), C.c_void_p(cache.table.data_ptr()),
+                                                   cache.max_pages, C.c_void_p(seq_lens.data_ptr()), max_seq_len,
+                                                   scale, decay, C.c_void_p(mass.data_ptr()), mass.shape[2],
+                                                   C.c_void_p(out.data_ptr()), dtype_code(out),
+                                                   C.c_void_p(workspace.data_ptr()), workspace.numel(),
+                                                   _stream_ptr(stream)), "decode_attention_mass_paged")
+
+
+def _evict_shapes(mass, mass_out, kept, seq_lens, new_lens, keep, h_kv):
+    import torch
+    B_ = mass.shape[0]
+    assert mass.dtype == torch.float32 and mass.is_contiguous() and mass.shape[1] == h_kv
+    assert mass_out.dtype == torch.float32 and mass_out.is_contiguous() and tuple(mass_out.shape[:2]) == (B_, h_kv)
+    assert kept.dtype == torch.int32 and kept.is_contiguous() and tuple(kept.shape) == (B_, h_kv, keep)
+    for t in (seq_lens, new_lens):
+        assert t.dtype == torch.int32 and t.is_contiguous() and t.numel() == B_
+    return B_
+
+
+def cache_evict(layout: Layout, src, seq_lens, src_capacity: int, max_seq_len: int, mass, keep: int, n_sink: int,
+                n_recent: int, dst, dst_capacity: int, mass_out, kept, new_lens, h_kv: int, stream=None):
+    """Copies the `keep` tokens of each (row, KV head) with the largest mass [B, h_kv, >=
+    max_seq_len] (the first n_sink and the last n_recent always) from the packed cache src
+    into dst, in their order. mass_out [B, h_kv, ld] fp32 receives their mass (then zeros),
+    kept [B, h_kv, keep] int32 their old positions (then -1), new_lens [B] int32 the lengths."""
+    B_ = _evict_shapes(mass, mass_out, kept, seq_lens, new_lens, keep, h_kv)
+    _check(load().bgtq_cache_evict(layout.handle, B_, h_kv, C.c_void_p(src.data_ptr()), src_capacity,
+                                   C.c_void_p(seq_lens.data_ptr()), max_seq_len, C.c_void_p(mass.data_ptr()),
+                                   mass.shape[2], keep, n_sink, n_recent, C.c_void_p(dst.data_ptr()), dst_capacity,
+                                   C.c_void_p(mass_out.data_ptr()), mass_out.shape[2], C.c_void_p(kept.data_ptr()),
+                                   C.c_void_p(new_lens.data_ptr()), _stream_ptr(stream)), "cache_evict")
+
+
+def cache_evict_paged(layout: Layout, src: PagedCache, seq_lens, max_seq_len: int, mass, keep: int, n_sink: int,
+                      n_recent: int, dst: PagedCache, mass_out, kept, new_lens, h_kv: int, stream=None):
+    B_ = _evict_shapes(mass, mass_out, kept, seq_lens, new_lens, keep, h_kv)
+    assert src.table.shape[0] == B_ and dst.table.shape[0] == B_
+    _check(load().bgtq_cache_evict_paged(layout.handle, B_, h_kv, C.c_void_p(src.pool.data_ptr()),
+                                         src.num_pages(layout, h_kv), C.c_void_p(src.table.data_ptr()), src.max_pages,
+                                         C.c_void_p(seq_lens.data_ptr()), max_seq_len, C.c_void_p(mass.data_ptr()),
+                                         mass.shape[2], keep, n_sink, n_recent, C.c_void_p(dst.pool.data_ptr()),
+                                         dst.num_pages(layout, h_kv), C.c_void_p(dst.table.data_ptr()), dst.max_pages,
+                                         C.c_void_p(mass_out.data_ptr()), mass_out.shape[2],
+                                         C.c_void_p(kept.data_ptr()), C.c_void_p(new_lens.data_ptr()),
+                                         _stream_ptr(stream)), "cache_evict_paged")

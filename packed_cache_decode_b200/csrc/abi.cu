@@ -793,3 +793,282 @@ bgtq_status bgtq_layout_set_status(const bgtq_layout_set* S, unsigned* flags, in
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------------ drafted trees, bounded cache
+namespace {
+
+bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
+  return x < y + nb && y < x + na;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<size_t>(p) & 15) == 0; }
+
+bgtq_status check_unaliased_lens(const std::string& w, const int* seq_lens, const int* new_lens, int batch) {
+  if (!seq_lens || !new_lens) return fail(BGTQ_ERR_INVALID, w + ": null pointer");
+  if (overlaps(seq_lens, size_t(batch) * 4, new_lens, size_t(batch) * 4))
+    return fail(BGTQ_ERR_INVALID, w + ": new_lens must not overlap seq_lens");
+  return BGTQ_OK;
+}
+
+bgtq_status commit_impl(const DevLayout& D, const char* who, const int* path, int path_ld, const int* n_path,
+                        const int* n_nodes, int n_q, int batch, int h_kv, const CacheRef& c, const int* seq_lens,
+                        int* new_lens, void* stream) {
+  const std::string w(who);
+  if (batch <= 0 || h_kv <= 0 || (long long)batch * h_kv > 0x7fffffffLL)
+    return fail(BGTQ_ERR_INVALID, w + ": bad batch / h_kv");
+  if (n_q < 1 || n_q > BGTQ_MAX_TREE) return fail(BGTQ_ERR_INVALID, w + ": n_q must be 1..64");
+  if (path_ld < n_q) return fail(BGTQ_ERR_INVALID, w + ": path_ld must be at least n_q");
+  if (!path || !n_path) return fail(BGTQ_ERR_INVALID, w + ": null pointer");
+  if (!aligned16(c.base)) return fail(BGTQ_ERR_INVALID, w + ": cache not 16-byte aligned");
+  bgtq_status st = check_unaliased_lens(w, seq_lens, new_lens, batch);
+  if (st != BGTQ_OK) return st;
+  cudaError_t e = launch_commit(D, batch, h_kv, path, path_ld, n_path, n_nodes, n_q, c, seq_lens, new_lens,
+                                static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? BGTQ_OK : cuda_fail(e, who);
+}
+
+// Shape limits of a tree call; what does not fit is refused by both the workspace query and
+// the call.
+bool tree_shape(int batch, int n_q, int h_q, int h_kv, long long max_seq_len) {
+  if (batch <= 0 || h_kv <= 0 || h_q <= 0 || h_q % h_kv || h_q / h_kv > kMaxCols) return false;
+  if (n_q < 1 || n_q > BGTQ_MAX_TREE || max_seq_len < 0) return false;
+  const long long ct = ((long long)(h_q / h_kv) * n_q + kMaxG - 1) / kMaxG;
+  return (long long)batch * h_kv * ct <= 0x7fffffffLL / (kMaxG * 2);
+}
+
+// Query columns of a KV head (node x query head) from which a tree call takes the tcgen05
+// kernel (128 columns per unit) instead of the decode kernel's 8-column tiles.
+constexpr int kTreeMinCols = 17;
+bool tree_wide(int h_q, int h_kv, int n_q) { return (h_q / h_kv) * n_q >= kTreeMinCols; }
+
+size_t tree_workspace(int batch, int h_q, int h_kv, int n_q, long long max_seq_len, int sms) {
+  return tree_wide(h_q, h_kv, n_q) ? plan_tree(batch, h_q, h_kv, n_q, max_seq_len, sms).workspace_bytes
+                                   : plan_decode(batch, h_q * n_q, h_kv, max_seq_len, sms).workspace_bytes;
+}
+
+bgtq_status tree_impl(const DevLayout& D, const char* who, const void* q, int q_dtype, int batch, int n_q, int h_q,
+                      int h_kv, const unsigned long long* mask, const int* n_nodes, const CacheRef& c,
+                      const int* seq_lens, long long max_seq_len, float softmax_scale, void* out, int out_dtype,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  const std::string w(who);
+  if (!valid_dtype(q_dtype) || !valid_dtype(out_dtype)) return fail(BGTQ_ERR_INVALID, w + ": bad dtype");
+  if (!tree_shape(batch, n_q, h_q, h_kv, max_seq_len))
+    return fail(BGTQ_ERR_INVALID, w + ": need h_q = G * h_kv with G in 1..32, n_q in 1..64 and a batch that fits");
+  if (max_seq_len > c.n_tiles * kTile) return fail(BGTQ_ERR_CAPACITY, w + ": max_seq_len must be in [0, capacity]");
+  if (!std::isfinite(softmax_scale)) return fail(BGTQ_ERR_INVALID, w + ": bad softmax_scale");
+  if (!q || !mask || !seq_lens || !out) return fail(BGTQ_ERR_INVALID, w + ": null pointer");
+  if (!aligned16(c.base)) return fail(BGTQ_ERR_INVALID, w + ": cache not 16-byte aligned");
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, who);
+  const size_t need = tree_workspace(batch, h_q, h_kv, n_q, max_seq_len, sms);
+  if (!workspace || workspace_bytes < need)
+    return fail(BGTQ_ERR_WORKSPACE, w + ": workspace missing or smaller than bgtq_tree_workspace_bytes()");
+  if ((reinterpret_cast<size_t>(workspace) & 255) != 0)
+    return fail(BGTQ_ERR_WORKSPACE, w + ": workspace not 256-byte aligned");
+  const TreeArgs tree{mask, n_nodes};
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (tree_wide(h_q, h_kv, n_q))
+    e = launch_tree(D, plan_tree(batch, h_q, h_kv, n_q, max_seq_len, sms), q, q_dtype, batch, h_q, h_kv, n_q, tree, c,
+                    seq_lens, max_seq_len, softmax_scale, out, out_dtype, workspace, s);
+  else
+    e = launch_tree_columns(D, plan_decode(batch, h_q * n_q, h_kv, max_seq_len, sms), q, q_dtype, batch, h_q, h_kv, n_q,
+                            tree, c, seq_lens, softmax_scale, out, out_dtype, workspace, s);
+  return e == cudaSuccess ? BGTQ_OK : cuda_fail(e, who);
+}
+
+bgtq_status mass_impl(const DevLayout& D, const char* who, const void* q, int q_dtype, int batch, int h_q, int h_kv,
+                      const CacheRef& c, const int* seq_lens, long long max_seq_len, float softmax_scale, float decay,
+                      float* mass, long long mass_ld, void* out, int out_dtype, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  const std::string w(who);
+  DecodePlan plan;
+  bgtq_status st = attention_checks(who, q_dtype, batch, h_q, h_kv, 1, c.n_tiles * kTile, max_seq_len, softmax_scale,
+                                    q, seq_lens, out, workspace, workspace_bytes, &plan);
+  if (st != BGTQ_OK) return st;
+  if (!valid_dtype(out_dtype)) return fail(BGTQ_ERR_INVALID, w + ": bad out_dtype");
+  if (!mass) return fail(BGTQ_ERR_INVALID, w + ": null pointer");
+  if (mass_ld < max_seq_len) return fail(BGTQ_ERR_INVALID, w + ": mass_ld must be at least max_seq_len");
+  if (!std::isfinite(decay)) return fail(BGTQ_ERR_INVALID, w + ": bad decay");
+  if (!aligned16(c.base)) return fail(BGTQ_ERR_INVALID, w + ": cache not 16-byte aligned");
+  if ((reinterpret_cast<size_t>(workspace) & 255) != 0)
+    return fail(BGTQ_ERR_WORKSPACE, w + ": workspace not 256-byte aligned");
+  if (workspace_bytes < (plan.workspace_bytes + 255) / 256 * 256 + mass_logits_bytes(batch, h_q, plan))
+    return fail(BGTQ_ERR_WORKSPACE, w + ": workspace smaller than bgtq_mass_workspace_bytes()");
+  cudaError_t e = launch_decode_mass(D, plan, q, q_dtype, batch, h_q, h_kv, c, seq_lens, softmax_scale, decay, mass,
+                                     mass_ld, out, out_dtype, workspace, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? BGTQ_OK : cuda_fail(e, who);
+}
+
+bgtq_status evict_impl(const DevLayout& D, const char* who, int batch, int h_kv, const CacheRef& src,
+                       const int* seq_lens, long long max_seq_len, const float* mass, long long mass_ld, int keep,
+                       int n_sink, int n_recent, const CacheRef& dst, float* mass_out, long long mass_out_ld,
+                       int* kept, int* new_lens, void* stream) {
+  const std::string w(who);
+  if (batch <= 0 || h_kv <= 0 || (long long)batch * h_kv > 65535)
+    return fail(BGTQ_ERR_INVALID, w + ": need 1 <= batch * h_kv <= 65535");
+  if (keep < 1 || n_sink < 0 || n_recent < 0 || (long long)n_sink + n_recent > keep)
+    return fail(BGTQ_ERR_INVALID, w + ": need keep >= 1 and 0 <= n_sink + n_recent <= keep");
+  if (max_seq_len < 0 || max_seq_len > src.n_tiles * kTile || max_seq_len > (1LL << 30))
+    return fail(BGTQ_ERR_CAPACITY, w + ": max_seq_len must be in [0, capacity] and at most 2^30");
+  const long long most = std::min<long long>(keep, max_seq_len);
+  if (dst.n_tiles * kTile < most) return fail(BGTQ_ERR_CAPACITY, w + ": the destination holds fewer tokens than are kept");
+  if (!mass || !mass_out || !kept) return fail(BGTQ_ERR_INVALID, w + ": null pointer");
+  if (mass_ld < max_seq_len || mass_out_ld < most)
+    return fail(BGTQ_ERR_INVALID, w + ": mass_ld or mass_out_ld smaller than the tokens it must hold");
+  bgtq_status st = check_unaliased_lens(w, seq_lens, new_lens, batch);
+  if (st != BGTQ_OK) return st;
+  const size_t units = size_t(batch) * h_kv;
+  if (overlaps(mass, units * mass_ld * 4, mass_out, units * mass_out_ld * 4))
+    return fail(BGTQ_ERR_INVALID, w + ": mass_out must not overlap mass");
+  if (!aligned16(src.base) || !aligned16(dst.base)) return fail(BGTQ_ERR_INVALID, w + ": cache not 16-byte aligned");
+  if (!src.table && !dst.table && overlaps(src.base, units * src.n_tiles * D.tile_bytes, dst.base, units * dst.n_tiles * D.tile_bytes))
+    return fail(BGTQ_ERR_INVALID, w + ": the destination must not overlap the source");
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess)
+    e = launch_evict(D, batch, h_kv, src, seq_lens, max_seq_len, mass, mass_ld, keep, n_sink, n_recent, dst, mass_out,
+                     mass_out_ld, kept, new_lens, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? BGTQ_OK : cuda_fail(e, who);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t bgtq_tree_workspace_bytes(const bgtq_layout* L, int batch, int h_q, int h_kv, int n_q,
+                                 long long max_seq_len) {
+  if (!L || !tree_shape(batch, n_q, h_q, h_kv, max_seq_len)) {
+    set_error("tree_workspace_bytes: bad arguments");
+    return 0;
+  }
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    set_error("tree_workspace_bytes: no CUDA device");
+    return 0;
+  }
+  return tree_workspace(batch, h_q, h_kv, n_q, max_seq_len, sms);
+}
+
+bgtq_status bgtq_tree_attention(const bgtq_layout* L, const void* q, int q_dtype, int batch, int n_q, int h_q,
+                                int h_kv, const unsigned long long* tree_mask_dev, const int* n_nodes_dev,
+                                const void* cache, const int* seq_lens_dev, long long capacity, long long max_seq_len,
+                                float softmax_scale, void* out, int out_dtype, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  bgtq_status st = check_device(L, "tree_attention");
+  CacheRef c{};
+  if (st == BGTQ_OK) st = contiguous("tree_attention", const_cast<void*>(cache), capacity, &c);
+  if (st != BGTQ_OK) return st;
+  return tree_impl(L->dev, "tree_attention", q, q_dtype, batch, n_q, h_q, h_kv, tree_mask_dev, n_nodes_dev, c,
+                   seq_lens_dev, max_seq_len, softmax_scale, out, out_dtype, workspace, workspace_bytes, stream);
+}
+
+bgtq_status bgtq_tree_attention_paged(const bgtq_layout* L, const void* q, int q_dtype, int batch, int n_q, int h_q,
+                                      int h_kv, const unsigned long long* tree_mask_dev, const int* n_nodes_dev,
+                                      const void* pool, long long num_pages, const int* block_table_dev,
+                                      long long max_pages, const int* seq_lens_dev, long long max_seq_len,
+                                      float softmax_scale, void* out, int out_dtype, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  bgtq_status st = check_device(L, "tree_attention_paged");
+  CacheRef c{};
+  if (st == BGTQ_OK)
+    st = paged("tree_attention_paged", const_cast<void*>(pool), num_pages, block_table_dev, max_pages, &c);
+  if (st != BGTQ_OK) return st;
+  return tree_impl(L->dev, "tree_attention_paged", q, q_dtype, batch, n_q, h_q, h_kv, tree_mask_dev, n_nodes_dev, c,
+                   seq_lens_dev, max_seq_len, softmax_scale, out, out_dtype, workspace, workspace_bytes, stream);
+}
+
+bgtq_status bgtq_tree_commit(const bgtq_layout* L, const int* path_dev, int path_ld, const int* n_path_dev,
+                             const int* n_nodes_dev, int n_q, int batch, int h_kv, void* cache,
+                             const int* seq_lens_dev, int* new_lens_dev, long long capacity, void* stream) {
+  bgtq_status st = check_device(L, "tree_commit");
+  CacheRef c{};
+  if (st == BGTQ_OK) st = contiguous("tree_commit", cache, capacity, &c);
+  if (st != BGTQ_OK) return st;
+  return commit_impl(L->dev, "tree_commit", path_dev, path_ld, n_path_dev, n_nodes_dev, n_q, batch, h_kv, c,
+                     seq_lens_dev, new_lens_dev, stream);
+}
+
+bgtq_status bgtq_tree_commit_paged(const bgtq_layout* L, const int* path_dev, int path_ld, const int* n_path_dev,
+                                   const int* n_nodes_dev, int n_q, int batch, int h_kv, void* pool,
+                                   long long num_pages, const int* block_table_dev, long long max_pages,
+                                   const int* seq_lens_dev, int* new_lens_dev, void* stream) {
+  bgtq_status st = check_device(L, "tree_commit_paged");
+  CacheRef c{};
+  if (st == BGTQ_OK) st = paged("tree_commit_paged", pool, num_pages, block_table_dev, max_pages, &c);
+  if (st != BGTQ_OK) return st;
+  return commit_impl(L->dev, "tree_commit_paged", path_dev, path_ld, n_path_dev, n_nodes_dev, n_q, batch, h_kv, c,
+                     seq_lens_dev, new_lens_dev, stream);
+}
+
+size_t bgtq_mass_workspace_bytes(const bgtq_layout* L, int batch, int h_q, int h_kv, long long max_seq_len) {
+  const size_t base = bgtq_workspace_bytes(L, batch, h_q, h_kv, max_seq_len);
+  if (!base) return 0;
+  DecodePlan p{};
+  p.max_tiles = int(std::max<long long>(1, (max_seq_len + kTile - 1) / kTile));
+  return (base + 255) / 256 * 256 + mass_logits_bytes(batch, h_q, p);
+}
+
+bgtq_status bgtq_decode_attention_mass(const bgtq_layout* L, const void* q, int q_dtype, int batch, int h_q, int h_kv,
+                                       const void* cache, const int* seq_lens_dev, long long capacity,
+                                       long long max_seq_len, float softmax_scale, float decay, float* mass,
+                                       long long mass_ld, void* out, int out_dtype, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  bgtq_status st = check_device(L, "decode_attention_mass");
+  CacheRef c{};
+  if (st == BGTQ_OK) st = contiguous("decode_attention_mass", const_cast<void*>(cache), capacity, &c);
+  if (st != BGTQ_OK) return st;
+  return mass_impl(L->dev, "decode_attention_mass", q, q_dtype, batch, h_q, h_kv, c, seq_lens_dev, max_seq_len,
+                   softmax_scale, decay, mass, mass_ld, out, out_dtype, workspace, workspace_bytes, stream);
+}
+
+bgtq_status bgtq_decode_attention_mass_paged(const bgtq_layout* L, const void* q, int q_dtype, int batch, int h_q,
+                                             int h_kv, const void* pool, long long num_pages,
+                                             const int* block_table_dev, long long max_pages, const int* seq_lens_dev,
+                                             long long max_seq_len, float softmax_scale, float decay, float* mass,
+                                             long long mass_ld, void* out, int out_dtype, void* workspace,
+                                             size_t workspace_bytes, void* stream) {
+  bgtq_status st = check_device(L, "decode_attention_mass_paged");
+  CacheRef c{};
+  if (st == BGTQ_OK)
+    st = paged("decode_attention_mass_paged", const_cast<void*>(pool), num_pages, block_table_dev, max_pages, &c);
+  if (st != BGTQ_OK) return st;
+  return mass_impl(L->dev, "decode_attention_mass_paged", q, q_dtype, batch, h_q, h_kv, c, seq_lens_dev, max_seq_len,
+                   softmax_scale, decay, mass, mass_ld, out, out_dtype, workspace, workspace_bytes, stream);
+}
+
+bgtq_status bgtq_cache_evict(const bgtq_layout* L, int batch, int h_kv, const void* src, long long src_capacity,
+                             const int* seq_lens_dev, long long max_seq_len, const float* mass, long long mass_ld,
+                             int keep, int n_sink, int n_recent, void* dst, long long dst_capacity, float* mass_out,
+                             long long mass_out_ld, int* kept_dev, int* new_lens_dev, void* stream) {
+  bgtq_status st = check_device(L, "cache_evict");
+  CacheRef s{}, d{};
+  if (st == BGTQ_OK) st = contiguous("cache_evict (source)", const_cast<void*>(src), src_capacity, &s);
+  if (st == BGTQ_OK) st = contiguous("cache_evict (destination)", dst, dst_capacity, &d);
+  if (st != BGTQ_OK) return st;
+  return evict_impl(L->dev, "cache_evict", batch, h_kv, s, seq_lens_dev, max_seq_len, mass, mass_ld, keep, n_sink,
+                    n_recent, d, mass_out, mass_out_ld, kept_dev, new_lens_dev, stream);
+}
+
+bgtq_status bgtq_cache_evict_paged(const bgtq_layout* L, int batch, int h_kv, const void* src_pool,
+                                   long long src_pages, const int* src_table_dev, long long src_max_pages,
+                                   const int* seq_lens_dev, long long max_seq_len, const float* mass,
+                                   long long mass_ld, int keep, int n_sink, int n_recent, void* dst_pool,
+                                   long long dst_pages, const int* dst_table_dev, long long dst_max_pages,
+                                   float* mass_out, long long mass_out_ld, int* kept_dev, int* new_lens_dev,
+                                   void* stream) {
+  bgtq_status st = check_device(L, "cache_evict_paged");
+  CacheRef s{}, d{};
+  if (st == BGTQ_OK)
+    st = paged("cache_evict_paged (source)", const_cast<void*>(src_pool), src_pages, src_table_dev, src_max_pages, &s);
+  if (st == BGTQ_OK)
+    st = paged("cache_evict_paged (destination)", dst_pool, dst_pages, dst_table_dev, dst_max_pages, &d);
+  if (st != BGTQ_OK) return st;
+  return evict_impl(L->dev, "cache_evict_paged", batch, h_kv, s, seq_lens_dev, max_seq_len, mass, mass_ld, keep,
+                    n_sink, n_recent, d, mass_out, mass_out_ld, kept_dev, new_lens_dev, stream);
+}
+
+}  // extern "C"

@@ -58,4 +58,53 @@ cudaError_t launch_scores(const DevLayout& L, const DecodePlan& plan, const void
                           int h_kv, const CacheRef& cache, const int* seq_lens, float softmax_scale, float* scores,
                           long long scores_ld, void* workspace, cudaStream_t stream, const DevLayout* heads = nullptr);
 
+// Drafted trees of a call: mask [batch][n_q] words (bit i of node j: it sees node i),
+// n_nodes [batch] (null: n_q nodes in every row).
+struct TreeArgs {
+  const unsigned long long* mask;
+  const int* n_nodes;
+};
+// Attention of the rows' drafted trees, 8 query columns (node x head) per tensor-core tile
+// of the decode kernel: the plan is made for h_q n_q columns, each column tile reads the
+// KV head's cache once.
+cudaError_t launch_tree_columns(const DevLayout& L, const DecodePlan& plan, const void* q, int q_dtype, int batch,
+                                int h_q, int h_kv, int n_q, const TreeArgs& tree, const CacheRef& cache,
+                                const int* seq_lens, float softmax_scale, void* out, int out_dtype, void* workspace,
+                                cudaStream_t stream);
+
+// The same for many query columns: 128 columns per unit on tcgen05 (tree_attention.cu).
+// Workspace: offsets of its parts and its size.
+struct TreePlan {
+  int col_tiles, n_ctas;
+  long long units;
+  size_t prefix_at, q_at, scale_at, ml_at, o_at, workspace_bytes;
+};
+TreePlan plan_tree(int batch, int h_q, int h_kv, int n_q, long long max_seq_len, int num_sms);
+cudaError_t launch_tree(const DevLayout& L, const TreePlan& plan, const void* q, int q_dtype, int batch, int h_q,
+                        int h_kv, int n_q, const TreeArgs& tree, const CacheRef& cache, const int* seq_lens,
+                        long long max_seq_len, float softmax_scale, void* out, int out_dtype, void* workspace,
+                        cudaStream_t stream);
+
+// Decode attention that also keeps an attention mass: mass[(b h_kv + h) mass_ld + t] =
+// decay x itself + the weight of cached token t summed over the query heads of KV head h.
+// The workspace is the plan's (rounded up to 256 bytes) followed by mass_logits_bytes().
+size_t mass_logits_bytes(int batch, int h_q, const DecodePlan& plan);
+cudaError_t launch_decode_mass(const DevLayout& L, const DecodePlan& plan, const void* q, int q_dtype, int batch,
+                               int h_q, int h_kv, const CacheRef& cache, const int* seq_lens, float softmax_scale,
+                               float decay, float* mass, long long mass_ld, void* out, int out_dtype, void* workspace,
+                               cudaStream_t stream);
+
+// The accepted path of each row's drafted tree, moved to the end of the prefix (token
+// L - n + path[i] to L - n + i), and the rows' new lengths.
+cudaError_t launch_commit(const DevLayout& L, int batch, int h_kv, const int* path, int path_ld, const int* n_path,
+                          const int* n_nodes, int n_q, const CacheRef& cache, const int* seq_lens, int* new_lens,
+                          cudaStream_t stream);
+
+// Eviction into another cache: the keep tokens of each (row, KV head) with the largest
+// mass, the first n_sink and the last n_recent always, in their order.
+cudaError_t launch_evict(const DevLayout& L, int batch, int h_kv, const CacheRef& src, const int* seq_lens,
+                         long long max_seq_len, const float* mass, long long mass_ld, int keep, int n_sink,
+                         int n_recent, const CacheRef& dst, float* mass_out, long long mass_out_ld, int* kept,
+                         int* new_lens, int num_sms, cudaStream_t stream);
+
 }  // namespace bgtq
