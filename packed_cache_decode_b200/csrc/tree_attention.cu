@@ -21,17 +21,18 @@
 //
 // One CTA per SM takes an equal slice of the units' tiles (64 tokens) laid end to end, units
 // being (row, KV head, 128 columns); rows count by their true lengths, which a prefix sum
-// made by the preparation kernel tells. 16 warps:
-//  * warp 13: bulk copies of packed tiles into a ring;
-//  * warps 14-15: the tile's norms: scaled hi + lo pairs for the keys, fp32 for the values;
-//  * warps 4-11: decode codes into K hi, K lo and V operands in shared memory (two
+// made by the preparation kernel tells. 20 warps:
+//  * warp 17: bulk copies of packed tiles into a ring;
+//  * warps 18-19: the tile's norms: scaled hi + lo pairs for the keys, fp32 for the values;
+//  * warps 8-15: decode codes into K hi, K lo and V operands in shared memory (two
 //    buffers). A quad of a lane's code string is exactly one 16-byte row of a K-major core
 //    matrix (8 tokens x 8 dims), so every store of a warp is 128 consecutive bytes;
-//  * warp 12: issues the matrix instructions, Q' and P from tensor memory, K and V from
+//  * warp 16: issues the matrix instructions, Q' and P from tensor memory, K and V from
 //    shared memory: QK of tile i + 1, then PV of tile i;
-//  * warps 0-3: softmax, one thread per column: S from tensor memory, P back to it. The
-//    reference maximum moves only when a tile exceeds it by 2^3 (fp16 holds P while |v| /
-//    sqrt(128) stays below 8000), so O is seldom rescaled; the sums are right either way.
+//  * warps 0-7: softmax, one thread per column, two groups that take tiles in turn: S from tensor memory, P back to it. The
+//    columns' reference sits 2^5 above the maximum it was set by and moves only when a tile
+//    exceeds it by 2^3 (fp16 holds P while |v| / sqrt(128) stays below 8000), so O is seldom
+//    rescaled; the sums are right either way.
 // Q' lives in tensor memory because an M = 128, N = 64 product reading both operands from
 // shared memory would need 192 bytes per cycle of it, above the 128 there are.
 // Tensor memory columns: Q' hi and lo (up to 160), S 2 x 64, P 2 x 32, O 128.
@@ -51,18 +52,21 @@ namespace bgtq {
 
 namespace {
 
-constexpr int kTreeThreads = 512;
+constexpr int kTreeThreads = 640;
 constexpr int kCols = 128;                // query columns of a unit (rows of the matrix products)
-constexpr int kDecWarp0 = 4, kDecWarps = 8;
-constexpr int kMmaWarp = 12, kLoadWarp = 13, kNormWarp0 = 14;
+constexpr int kSoftWarps = 8, kDecWarp0 = 8, kDecGroup = 4;  // decode: two groups of kDecGroup warps
+constexpr int kMmaWarp = kDecWarp0 + 2 * kDecGroup, kLoadWarp = kMmaWarp + 1, kNormWarp0 = kMmaWarp + 2;
+static_assert(32 * (kNormWarp0 + 2) == kTreeThreads && kDecGroup == 4, "warps; a decode warp per value chunk");
 constexpr int kMaxStages = 4;
 constexpr int kMetas = 8;                 // tiles between the norm warps and the softmax: stages + 2 at most
 constexpr int kMaxDims = 160;             // packed dims as quads: kMaxQuads x 8
 constexpr int kTmemS = 160, kTmemP = 288, kTmemO = 352;
-constexpr unsigned kTreeWaitLimit = 1u << 20;
-// key norms of a tile as the decode warps use them: per group 64 entries (slot-major) of
-// (hi, hi, lo, lo) fp16
+constexpr unsigned kTreeWaitRounds = 1u << 12, kTreeSuspend = 10000u;  // rounds of 256 tries, nanoseconds of a try
+// key norms of a tile as the decode warps use them: per group and slot pair (tokens g + 16 p
+// and g + 16 p + 8) the rows' (hi, hi, lo, lo) fp16 of both slots, 128 consecutive bytes
 constexpr int kNormBytes = kMaxGroups * kTile * 8;
+// what a decode lane needs of a key quad: code offset in the tile, norm offset
+constexpr int kUnitBytes = kMaxQuads * 32 * 8;
 
 struct TreeLaunch {
   CacheRef cache;
@@ -121,11 +125,16 @@ __device__ __forceinline__ void tc_ld32(unsigned (&v)[32], unsigned addr) {
       : BGTQ_R8(v, 0), BGTQ_R8(v, 8), BGTQ_R8(v, 16), BGTQ_R8(v, 24)
       : "r"(addr));
 }
-__device__ __forceinline__ void tc_st32(unsigned addr, const unsigned (&v)[32]) {
+__device__ __forceinline__ void tc_ld16(unsigned (&v)[16], unsigned addr) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-      BGTQ_W8(v, 0), BGTQ_W8(v, 8), BGTQ_W8(v, 16), BGTQ_W8(v, 24)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : BGTQ_R8(v, 0), BGTQ_R8(v, 8)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_st16(unsigned addr, const unsigned (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      BGTQ_W8(v, 0), BGTQ_W8(v, 8)
       : "memory");
 }
 __device__ __forceinline__ void tc_st4(unsigned addr, const uint4& v) {
@@ -151,6 +160,7 @@ struct TreeWalk {
     at = c < C ? c * T / C : 0;
     end = c < C ? (c + 1) * T / C : 0;
     int lo = 0, hi = a.batch;  // the row whose range holds `at`
+#pragma unroll 1
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (a.prefix[mid] <= at) lo = mid;
@@ -160,6 +170,7 @@ struct TreeWalk {
   }
   __device__ __forceinline__ bool next(const TreeLaunch& a) {
     if (at >= end) return false;
+#pragma unroll 1
     while (a.prefix[b + 1] <= at) ++b;
     const long long p0 = a.prefix[b];
     nt = int((a.prefix[b + 1] - p0) / a.row_units);
@@ -180,68 +191,153 @@ __device__ __forceinline__ long long tree_row_len(const TreeLaunch& a, int b) {
 
 struct TreeShared {
   unsigned long long full[kMaxStages], normed[kMaxStages], empty[kMaxStages];
-  unsigned long long kv_full[2], qk_done[2], p_full[2], pv_done[2], q_full, tables;
+  unsigned long long k_full[2], v_full[2], qk_done[2], p_full[2], pv_done[2], q_full, tables;
   unsigned tmem;
-  int abort;
+  int abort, dec_ok[2][2];
+  int range[kDecGroup][5][2];   // key quads of each decode warp, by rate
   int present[kMetas];
   float scale[kMetas][2];
   int valid[kMetas];
+  unsigned long long max_done[2][4], sum_done[4];
+  float mref[kCols];            // the columns' reference maximum
+  float total[2][kCols];        // the second group's sums at a unit's end (by unit parity)
   alignas(16) float vnorm[kMetas][kTile];   // |v| / (sqrt(128) kappa) by token (read four at a time)
 };
 
+// A position in the ring of stages: stage and parity of its current round.
+struct RingPos {
+  unsigned st = 0, round = 0;
+  __device__ __forceinline__ void step(unsigned n) {
+    if (++st == n) {
+      st = 0;
+      ++round;
+    }
+  }
+};
+
 // Waits (bounded) for the barrier's phase of the given parity; false once the CTA gives up.
+// The polling loop is kept short: the waiting warps share issue slots with the working ones.
 __device__ __forceinline__ bool tree_wait(TreeShared& s, unsigned long long* bar, unsigned parity) {
-  for (unsigned i = 0; i < kTreeWaitLimit; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
+  const unsigned addr = smem_addr(bar);
+#pragma unroll 1
+  for (unsigned i = 0; i < kTreeWaitRounds; ++i) {
+    unsigned left;
+    asm volatile(
+        "{\n .reg .pred p, q;\n"
+        " mov.u32 %0, 256;\n"
+        "AGAIN:\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " @p bra DONE;\n"
+        " sub.u32 %0, %0, 1;\n"
+        " setp.ne.u32 q, %0, 0;\n"
+        " @q bra AGAIN;\n"
+        "DONE:\n}\n"
+        : "=&r"(left)
+        : "r"(addr), "r"(parity), "r"(kTreeSuspend)
+        : "memory");
+    if (left) return true;
     if (*reinterpret_cast<volatile int*>(&s.abort)) return false;
   }
   *reinterpret_cast<volatile int*>(&s.abort) = 1;
   return false;
 }
+// The same for a role that runs ahead of the others: it sleeps between its tries.
+__device__ __forceinline__ bool tree_wait_patient(TreeShared& s, unsigned long long* bar, unsigned parity) {
+#pragma unroll 1
+  for (unsigned i = 0; i < kTreeWaitRounds * 64u; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(&s.abort)) return false;
+    __nanosleep(100);
+  }
+  *reinterpret_cast<volatile int*>(&s.abort) = 1;
+  return false;
+}
+__device__ __forceinline__ void group_barrier(int id) { asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(32 * kDecGroup) : "memory"); }
 
-// K operand words of one quad (rate R) for the lane's eight tokens: hi at kh + 128 m, lo at
-// kh + lo_off + 128 m. nrm: the lane's norm entries (4 x 16 bytes) of the quad's group.
-template <int R>
-__device__ __forceinline__ void decode_quad(unsigned tb, unsigned off, unsigned nrm, unsigned kh, unsigned lo_off,
-                                            unsigned t8, unsigned t3, unsigned c8) {
-  KCodes<R> c;
-  c.load(tb, off, false);
+// K operand words of one quad (rate R) from the lane's codes c, for its eight tokens: hi at
+// kh + 128 m, lo at kl + 128 m. nn: the lane's norms of the quad's group, (hi, lo) of slots 2j
+// and 2j + 1. All loads first, then the arithmetic; `next` runs in between (it fetches the next
+// quad's codes).
+template <int R, typename Next>
+__device__ __forceinline__ void decode_quad(const KCodes<R>& c, const uint4 (&nn)[4], unsigned kh, unsigned kl, unsigned t8,
+                                            unsigned t3, unsigned c8, Next&& next) {
+  unsigned ch[8], cl[8];
+  if constexpr (R == 2) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint4 nn = ld_s128(nrm + 16 * j);  // (hi, lo) of slots 2j and 2j + 1
-    uint2 e2 = make_uint2(0u, 0u);
-    if constexpr (R == 2) e2 = ld_s64(t8 + row8(c.w, c8, j));
+    for (int j = 0; j < 4; ++j) {
+      const uint2 e = ld_s64(t8 + row8(c.w, c8, j));
+      ch[2 * j] = e.x;
+      ch[2 * j + 1] = e.y;
+    }
+  } else if constexpr (R >= 3) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int m = 2 * j + i;
-      const unsigned nh = i ? nn.z : nn.x, nl = i ? nn.w : nn.y;
-      unsigned hi, lo;
-      if constexpr (R == 1) {
-        const unsigned sgn = (~c.w << (15 - m)) & 0x80008000u;  // code 0 is -1
-        hi = nh ^ sgn;
-        lo = nl ^ sgn;
-      } else {
-        unsigned ch, cl = 0;
-        if constexpr (R == 2) {
-          ch = i ? e2.y : e2.x;
-        } else {
-          uint2 e;
-          if constexpr (R == 3) e = ld_s64(t3 + c.row(m, c8));
-          else e = ld_s64(t8 + 128 + row8(m < 4 ? c.w.x : c.w.y, c8, m & 3));
-          ch = e.x;
-          cl = e.y;
-        }
-        const __half2 h = __hmul2(as_h2(ch), as_h2(nh));
-        __half2 l = __hfma2(as_h2(ch), as_h2(nh), __hneg2(h));
-        l = __hfma2(as_h2(ch), as_h2(nl), l);
-        if constexpr (R >= 3) l = __hfma2(as_h2(cl), as_h2(nh), l);
-        hi = as_u32(h);
-        lo = as_u32(l);
-      }
-      st_s32(kh + 128 * m, hi);
-      st_s32(kh + lo_off + 128 * m, lo);
+    for (int m = 0; m < 8; ++m) {
+      uint2 e;
+      if constexpr (R == 3) e = ld_s64(t3 + c.row(m, c8));
+      else e = ld_s64(t8 + 128 + row8(m < 4 ? c.w.x : c.w.y, c8, m & 3));
+      ch[m] = e.x;
+      cl[m] = e.y;
     }
   }
+  unsigned sgn0 = 0;
+  if constexpr (R == 1) sgn0 = ~c.w;
+  next();
+#pragma unroll
+  for (int m = 0; m < 8; ++m) {
+    const unsigned nh = m & 1 ? nn[m >> 1].z : nn[m >> 1].x, nl = m & 1 ? nn[m >> 1].w : nn[m >> 1].y;
+    unsigned hi, lo;
+    if constexpr (R == 1) {
+      const unsigned sgn = (sgn0 << (15 - m)) & 0x80008000u;  // code 0 is -1
+      hi = nh ^ sgn;
+      lo = nl ^ sgn;
+    } else {
+      const __half2 h = __hmul2(as_h2(ch[m]), as_h2(nh));
+      __half2 l = __hfma2(as_h2(ch[m]), as_h2(nh), __hneg2(h));
+      l = __hfma2(as_h2(ch[m]), as_h2(nl), l);
+      if constexpr (R >= 3) l = __hfma2(as_h2(cl[m]), as_h2(nh), l);
+      hi = as_u32(h);
+      lo = as_u32(l);
+    }
+    st_s32(kh + 128 * m, hi);
+    st_s32(kl + 128 * m, lo);
+  }
+}
+
+// Packed pairs of fp32 (one instruction for two lanes of arithmetic).
+__device__ __forceinline__ unsigned long long pack2(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(unsigned long long x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ bool elect_one() {
+  unsigned r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
 }
 
 template <int VR, bool NH>
@@ -258,21 +354,31 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
   const unsigned k_at = (base + kTbl + 127u) & ~127u;      // [2 buffers][hi, lo]
   const unsigned v_at = k_at + 4u * k_part;                // [2 buffers]
   const unsigned n_at = v_at + 2u * 16384u;                // norms [stage]
-  const unsigned r_at = n_at + unsigned(NS) * kNormBytes;  // ring [stage]
+  const unsigned u_at = n_at + unsigned(NS) * kNormBytes;  // key quads [quad][lane]
+  const unsigned r_at = u_at + kUnitBytes;                 // ring [stage]
 
   if (tid == 0) {
+#pragma unroll 1
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&s.full[i], 1);
       mbar_init(&s.normed[i], 2);
-      mbar_init(&s.empty[i], kDecWarps);
+      mbar_init(&s.empty[i], kDecGroup);
     }
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.kv_full[i], kDecWarps);
+      mbar_init(&s.k_full[i], kDecGroup);
+      mbar_init(&s.v_full[i], kDecGroup);
       mbar_init(&s.qk_done[i], 1);
-      mbar_init(&s.p_full[i], 4);
+      mbar_init(&s.p_full[i], kSoftWarps / 2);
       mbar_init(&s.pv_done[i], 1);
     }
-    mbar_init(&s.q_full, 4);
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s.max_done[0][i], 1);
+      mbar_init(&s.max_done[1][i], 1);
+      mbar_init(&s.sum_done[i], 1);
+    }
+    mbar_init(&s.q_full, kSoftWarps);
     mbar_init(&s.tables, 1);
     s.abort = 0;
     fence_mbar_init();
@@ -283,8 +389,46 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
   }
   // an odd last quad's partner stays zero (the products read it; its q' is zero too)
   if (nq & 1)
+#pragma unroll 1
     for (int i = tid; i < 4 * 256; i += kTreeThreads)
       st_s32(k_at + unsigned(i >> 8) * k_part + unsigned(nq) * 1024u + 4u * (i & 255), 0u);
+#pragma unroll 1
+  for (int it = warp; it < nq; it += kTreeThreads / 32) {
+    int gi = 0;
+#pragma unroll 1
+    while (gi + 1 < L.n_kgroups && it >= L.group_quad0[gi + 1]) ++gi;
+    const int r = L.group_rate[gi], P = L.quad_np[it], g = lane >> 2, t4 = lane & 3;
+    const unsigned li = t4 < P ? g * P + t4 : 0u;  // (a lane without a pair: any code, its q' is zero)
+    const unsigned qo = unsigned(L.quad_off[it]);
+    const unsigned off = r == 3 ? (qo + 4u * li) | ((qo + 32u * P + 2u * li) << 16) : qo + 2u * r * li;
+    st_s32(u_at + 8u * (it * 32 + lane), off);
+    st_s32(u_at + 8u * (it * 32 + lane) + 4u, unsigned(gi * kTile * 8 + 16 * g));
+  }
+  if (tid < kDecGroup) {
+    // the quads lie in descending rate; each decode warp takes a run of about equal cost
+    // (instructions per quad of rate 1..4), so that it and its partner in the other group,
+    // on the same scheduler, stay with the code of one or two rates
+    auto cost = [](int r) { return r == 1 ? 6 : r == 2 ? 7 : 11; };
+    auto rate_of = [&](int it) {
+      int gi = 0;
+#pragma unroll 1
+      while (gi + 1 < L.n_kgroups && it >= L.group_quad0[gi + 1]) ++gi;
+      return L.group_rate[gi];
+    };
+    int total = 0, run = 0;
+#pragma unroll 1
+    for (int it = 0; it < nq; ++it) total += cost(rate_of(it));
+#pragma unroll 1
+    for (int r = 0; r < 5; ++r) s.range[tid][r][0] = s.range[tid][r][1] = 0;
+#pragma unroll 1
+    for (int it = 0; it < nq; ++it) {
+      const int r = rate_of(it), c = cost(r), owner = min(kDecGroup - 1, (2 * run + c) * kDecGroup / (2 * total));
+      run += c;
+      if (owner != tid) continue;
+      if (s.range[tid][r][1] == 0) s.range[tid][r][0] = it;
+      s.range[tid][r][1] = it + 1;
+    }
+  }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   tc_fence_before();
   __syncthreads();
@@ -303,22 +447,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
     if (lane == 0) {
       const unsigned long long pol = evict_first_policy();
       unsigned i = 0;
+      RingPos r;
       bool go = true;
+#pragma unroll 1
       while (go && w.next(a)) {
         const int h = w.head(a);
-        for (int t = 0; t < w.n; ++t, ++i) {
-          const unsigned st = i % NS, round = i / NS;
-          if (round > 0 && !tree_wait(s, &s.empty[st], (round - 1) & 1u)) {
+#pragma unroll 1
+        for (int t = 0; t < w.n; ++t, ++i, r.step(NS)) {
+          if (r.round > 0 && !tree_wait_patient(s, &s.empty[r.st], (r.round - 1) & 1u)) {
             go = false;
             break;
           }
           const uint8_t* src = tile_ptr(a.cache, L, w.b, h, a.h_kv, w.lt0 + t);
           s.present[i % kMetas] = src != nullptr;
-          mbar_expect_tx(&s.full[st], src ? unsigned(TB) : 0u);
-          if (src) bulk_load(smem + (r_at - base) + st * TB, src, unsigned(TB), &s.full[st], pol);
+          mbar_expect_tx(&s.full[r.st], src ? unsigned(TB) : 0u);
+          if (src) bulk_load(smem + (r_at - base) + r.st * TB, src, unsigned(TB), &s.full[r.st], pol);
         }
       }
       // copies in flight land before the CTA ends: the last one of each stage
+#pragma unroll 1
       for (unsigned st = 0; st < unsigned(NS) && st < i; ++st) {
         const unsigned rounds = (i - 1 - st) / NS;
         mbar_wait_bounded(&s.full[st], rounds & 1u);
@@ -332,12 +479,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
     const int ng = L.n_kgroups;
     const float vscale = rsqrtf(float(kD)) / L.kappa_v;
     unsigned i = 0;
+    RingPos r;
     bool go = true;
+#pragma unroll 1
     while (go && w.next(a)) {
       const long long len = tree_row_len(a, w.b);
-      for (int t = 0; t < w.n; ++t, ++i) {
-        const unsigned st = i % NS, round = i / NS;
-        if (!__all_sync(0xffffffffu, tree_wait(s, &s.full[st], round & 1u))) {
+#pragma unroll 1
+      for (int t = 0; t < w.n; ++t, ++i, r.step(NS)) {
+        const unsigned st = r.st;
+        if (!__all_sync(0xffffffffu, tree_wait_patient(s, &s.full[st], r.round & 1u))) {
           go = false;
           break;
         }
@@ -352,24 +502,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
           }
           return x;
         };
-        float n[kMaxGroups], top = 0.f;
-#pragma unroll
-        for (int g = 0; g < kMaxGroups; ++g) {
-          n[g] = g < ng ? norm(g) : 0.f;
-          top = fmaxf(top, fabsf(n[g]));
-        }
+        float top = 0.f;
+#pragma unroll 1
+        for (int g = 0; g < ng; ++g) top = fmaxf(top, fabsf(norm(g)));
         const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
         const int ex = bits == 0u ? 127 : min(227, max(27, int(bits >> 23)));
         const float down = __int_as_float((254 - ex) << 23);
-#pragma unroll
-        for (int g = 0; g < kMaxGroups; ++g) {
-          if (g >= ng) break;
-          const float x = n[g] * down;
+#pragma unroll 1
+        for (int g = 0; g < ng; ++g) {
+          const float x = norm(g) * down;
           const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
           const unsigned hb = __half_as_ushort(hi), lb = __half_as_ushort(lo);
-          const unsigned at = dst + (g * kTile + entry) * 8;
-          st_s32(at, hb | hb << 16);
-          st_s32(at + 4, lb | lb << 16);
+          const unsigned at = dst + unsigned(g * kTile) * 8u + unsigned((tok >> 4) * 128 + (tok & 7) * 16 + (tok >> 3 & 1) * 8);
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hb | hb << 16), "r"(lb | lb << 16) : "memory");
         }
         s.vnorm[i % kMetas][tok] = norm(ng) * vscale;
         if (lane == 0) {
@@ -380,252 +525,359 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
         if (lane == 0) mbar_arrive(&s.normed[st]);
       }
     }
-  } else if (warp >= kDecWarp0 && warp < kDecWarp0 + kDecWarps) {
+  } else if (warp >= kDecWarp0 && warp < kMmaWarp) {
     const unsigned c8 = unsigned(lane & 15) << 3, lane4 = unsigned(lane) << 2;
-    const int g = lane >> 2, t4 = lane & 3;
-    bool go = __all_sync(0xffffffffu, tree_wait(s, &s.tables, 0u));
-    const unsigned t8 = launder(t8a), t3 = launder(t3a), vt = launder(vta);
+    // two groups take the tiles in turn (group = the operand buffer they fill)
+    const int dw = (warp - kDecWarp0) % kDecGroup, buf = (warp - kDecWarp0) / kDecGroup;
+    // (a timeout of the tables raises the flag that the waits below see)
+    tree_wait(s, &s.tables, 0u);
+    bool go = true;
+    const unsigned t8 = launder(t8a), t3 = launder(t3a), vt = launder(vta), units = launder(u_at) + 8u * lane;
+    const unsigned kb = k_at + buf * 2u * k_part + lane4;
     unsigned i = 0;
+    RingPos r;
+#pragma unroll 1
     while (go && w.next(a)) {
-      for (int t = 0; t < w.n; ++t, ++i) {
-        const unsigned st = i % NS, round = i / NS, buf = i & 1u, use = i >> 1;
-        bool ok = tree_wait(s, &s.full[st], round & 1u) && tree_wait(s, &s.normed[st], round & 1u);
-        if (use > 0) ok = ok && tree_wait(s, &s.qk_done[buf], (use - 1) & 1u) && tree_wait(s, &s.pv_done[buf], (use - 1) & 1u);
-        if (!__all_sync(0xffffffffu, ok)) {
+#pragma unroll 1
+      for (int t = 0; t < w.n; ++t, ++i, r.step(NS)) {
+        if ((i & 1u) != unsigned(buf)) continue;
+        const unsigned st = r.st, before = ((i >> 1) - 1u) & 1u;
+        // the group's first warp waits (bounded) for all of it and says how that went
+        if (dw == 0) {
+          bool ok = tree_wait(s, &s.full[st], r.round & 1u) && tree_wait(s, &s.normed[st], r.round & 1u);
+          if (i > 1) ok = ok && tree_wait(s, &s.qk_done[buf], before);
+          if (lane == 0) s.dec_ok[buf][0] = ok;
+        }
+        group_barrier(1 + buf);
+        /*dec:start*/
+        if (!*reinterpret_cast<volatile int*>(&s.dec_ok[buf][0])) {
           go = false;
           break;
         }
         const unsigned tb = launder(r_at + st * TB), nb = launder(n_at + st * kNormBytes);
-        const unsigned kb = k_at + buf * 2u * k_part + lane4, vb = v_at + buf * 16384u + lane4;
-        for (int it = warp - kDecWarp0; it < nq + 8; it += kDecWarps) {
-          if (it < nq) {
-            int gi = 0;
-            while (gi + 1 < L.n_kgroups && it >= L.group_quad0[gi + 1]) ++gi;
-            const int r = L.group_rate[gi], P = L.quad_np[it];
-            const unsigned li = t4 < P ? g * P + t4 : 0u;  // (a lane without a pair: any code, its q' is zero)
-            const unsigned qo = unsigned(L.quad_off[it]);
-            const unsigned nrm = nb + unsigned(gi * kTile + 8 * g) * 8u, kh = kb + unsigned(it) * 1024u;
-            switch (r) {
-              case 1: decode_quad<1>(tb, qo + 2u * li, nrm, kh, k_part, t8, t3, c8); break;
-              case 2: decode_quad<2>(tb, qo + 4u * li, nrm, kh, k_part, t8, t3, c8); break;
-              case 3: decode_quad<3>(tb, (qo + 4u * li) | ((qo + 32u * P + 2u * li) << 16), nrm, kh, k_part, t8, t3, c8); break;
-              default: decode_quad<4>(tb, qo + 8u * li, nrm, kh, k_part, t8, t3, c8); break;
-            }
-          } else {
-            const int v = it - nq, c = v >> 1, m0 = 4 * (v & 1);
-            ValueLane<VR> vl;
-            vl.load(tb + L.vcode_off + c * 256 * VR, lane);
-            auto dims = [&](auto first) {
+auto quads = [&](auto rate) {
+          constexpr int R = decltype(rate)::value;
+          // a quad's code offset has the alignment of its own rate, and the loads are pure: the
+          // launder() in here keeps them from being hoisted out of the branch on the rate
+          int it = s.range[dw][R][0];
+          const int last = s.range[dw][R][1];
+          if (it >= last) return;
+          KCodes<R> c;
+          uint2 q = ld_s64(units + 256u * launder(it));
+          c.load(tb, launder(q.x), false);
+          uint4 nn[4];  // one rate is one group: its norms serve all its quads
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int mt = decltype(first)::value + j;
-                unsigned x[4];
-                vl.regs(mt, t8, vt, c8, lane4, x);
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  st_s32(vb + unsigned((2 * c + (q >> 1)) * 16 + 2 * mt + (q & 1)) * 128u, x[q]);
-              }
-            };
-            if (m0 == 0) dims(IntC<0>{});
-            else dims(IntC<4>{});
+          for (int j = 0; j < 4; ++j) nn[j] = ld_s128(nb + q.y + 128 * j);
+#pragma unroll 1
+          for (; it < last; ++it) {
+            const unsigned kh = kb + unsigned(it) * 1024u;
+            KCodes<R> cn;
+            unsigned qn;
+            decode_quad<R>(c, nn, kh, kh + k_part, t8, t3, c8, [&] {
+              qn = ld_s32(units + 256u * launder(min(it + 1, last - 1)));
+              cn.load(tb, launder(qn), false);
+            });
+            c = cn;
           }
+        };
+        quads(IntC<4>{});
+        quads(IntC<3>{});
+        quads(IntC<2>{});
+        quads(IntC<1>{});
+        /*dec:k*/
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.k_full[buf]);
+        /*dec:kf*/
+        if (i > 1) {
+          if (dw == 0) {
+            const bool ok = tree_wait(s, &s.pv_done[buf], before);
+            if (lane == 0) s.dec_ok[buf][1] = ok;
+          }
+          group_barrier(1 + buf);
+          if (!*reinterpret_cast<volatile int*>(&s.dec_ok[buf][1])) {
+            go = false;
+            break;
+          }
+        }
+        /*dec:v*/
+        // values: warp dw takes chunk dw of the tile
+        const unsigned blk = tb + L.vcode_off + dw * 256 * VR, vb = v_at + buf * 16384u + lane4 + unsigned(dw) * 4096u;
+ValueLane<VR> vl;
+        vl.load(blk, lane);
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+          unsigned x[4];
+          vl.regs(mt, t8, vt, c8, lane4, x);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) st_s32(vb + unsigned(k >> 1) * 2048u + unsigned(2 * mt + (k & 1)) * 128u, x[k]);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&s.empty[st]);
-          mbar_arrive(&s.kv_full[buf]);
+          mbar_arrive(&s.v_full[buf]);
         }
+        /*dec:vf*/
       }
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      const unsigned id_s = tc_idesc(kCols, kTile), id_o = tc_idesc(kCols, kD);
-      const unsigned q_lo = unsigned(a.q_words);
-      auto scores = [&](unsigned i) {  // S of tile i
-        const unsigned buf = i & 1u, k0 = k_at + buf * 2u * k_part, d = tmem + kTmemS + 64u * buf;
-        for (int k = 0; k < steps; ++k) {
-          const unsigned long long hi = tc_desc(k0 + 2048u * k, 1024u, 128u), lo = tc_desc(k0 + k_part + 2048u * k, 1024u, 128u);
+    // the whole warp walks and waits, one elected lane issues
+    const unsigned id_s = tc_idesc(kCols, kTile), id_o = tc_idesc(kCols, kD);
+    const unsigned q_lo = unsigned(a.q_words);
+    auto scores = [&](unsigned i) {  // S of tile i
+      const unsigned buf = i & 1u, d = tmem + kTmemS + 64u * buf;
+      unsigned long long hi = tc_desc(k_at + buf * 2u * k_part, 1024u, 128u);
+      unsigned long long lo = tc_desc(k_at + buf * 2u * k_part + k_part, 1024u, 128u);
+      if (elect_one()) {
+#pragma unroll 2
+        for (int k = 0; k < steps; ++k, hi += 128u, lo += 128u) {  // (2048 bytes per step of 16 dims)
           tc_mma(d, tmem + 8u * k, hi, id_s, k > 0);
           tc_mma(d, tmem + q_lo + 8u * k, hi, id_s, true);
           tc_mma(d, tmem + 8u * k, lo, id_s, true);
         }
         tc_commit(&s.qk_done[buf]);
-      };
-      auto values = [&](unsigned i, bool first) {  // O += P V of tile i
-        const unsigned buf = i & 1u, v0 = v_at + buf * 16384u, p = tmem + kTmemP + 32u * buf;
-        for (int k = 0; k < 4; ++k) tc_mma(tmem + kTmemO, p + 8u * k, tc_desc(v0 + 4096u * k, 2048u, 128u), id_o, !first || k > 0);
+      }
+      __syncwarp();
+    };
+    auto values = [&](unsigned i, bool first) {  // O += P V of tile i
+      const unsigned buf = i & 1u, p = tmem + kTmemP + 32u * buf;
+      const unsigned long long v = tc_desc(v_at + buf * 16384u, 2048u, 128u);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tc_mma(tmem + kTmemO, p + 8u * k, v + 256u * k, id_o, !first || k > 0);
         tc_commit(&s.pv_done[buf]);
-      };
-      unsigned i = 0, seg = 0;
-      bool go = true;
-      while (go && w.next(a)) {
-        go = tree_wait(s, &s.q_full, seg++ & 1u) && tree_wait(s, &s.kv_full[i & 1u], (i >> 1) & 1u);
-        if (!go) break;
-        tc_fence_after();
-        scores(i);
-        for (int t = 0; t < w.n; ++t, ++i) {
-          if (t + 1 < w.n) {
-            if (!tree_wait(s, &s.kv_full[(i + 1) & 1u], ((i + 1) >> 1) & 1u)) {
-              go = false;
-              break;
-            }
-            tc_fence_after();
-            scores(i + 1);
-          }
-          if (!tree_wait(s, &s.p_full[i & 1u], (i >> 1) & 1u)) {
+      }
+      __syncwarp();
+    };
+    auto wait = [&](unsigned long long* bar, unsigned parity) {
+      const bool ok = __all_sync(0xffffffffu, tree_wait(s, bar, parity));
+      tc_fence_after();
+      return ok;
+    };
+    unsigned i = 0, seg = 0;
+    bool go = true;
+#pragma unroll 1
+    while (go && w.next(a)) {
+      go = wait(&s.q_full, seg++ & 1u) && wait(&s.k_full[i & 1u], (i >> 1) & 1u);
+      if (!go) break;
+      scores(i);
+#pragma unroll 1
+      for (int t = 0; t < w.n; ++t, ++i) {
+        if (t + 1 < w.n) {
+          if (!wait(&s.k_full[(i + 1) & 1u], ((i + 1) >> 1) & 1u)) {
             go = false;
             break;
           }
-          tc_fence_after();
-          values(i, t == 0);
+          scores(i + 1);
         }
+        if (!wait(&s.v_full[i & 1u], (i >> 1) & 1u) || !wait(&s.p_full[i & 1u], (i >> 1) & 1u)) {
+          go = false;
+          break;
+        }
+        values(i, t == 0);
       }
     }
   } else {
-    // softmax: thread = query column `tid` (lane `tid` of tensor memory)
-    const unsigned row = tmem + (unsigned(warp) << 21);  // lanes 32 warp ..
-    auto load_q = [&](long long u) {
-      const uint4* q = a.q + (size_t)u * (2 * a.q_words / 4) * kCols + tid;
-      for (int j = 0; j < 2 * a.q_words / 4; ++j) tc_st4(row + 4u * j, __ldg(q + (size_t)j * kCols));
+    // softmax: thread = query column; two groups of four warps take the tiles in turn. The
+    // reference maximum of a column passes from group to group: a group raises it for its
+    // tile only after the other did for the tile before (max_done, warp by warp), then both
+    // work on their exponentials at once. A group's sum follows the reference it last saw.
+    const unsigned grp = warp >> 2, quad = warp & 3;
+    const int c = tid & (kCols - 1);
+    const unsigned row = tmem + (quad << 21);  // lanes 32 quad ..
+    auto wait = [&](unsigned long long* bar, unsigned parity) {
+      return bool(__all_sync(0xffffffffu, tree_wait(s, bar, parity)));
+    };
+    auto load_q = [&](long long u) {  // this group's part of Q' (hi or lo)
+      const uint4* q = a.q + (size_t)(u * (2 * a.q_words / 4) + grp * (a.q_words / 4)) * kCols + c;
+      const unsigned at = row + grp * unsigned(a.q_words);
+      // q_words is a multiple of 8: groups of 2 x 4 words, their loads in flight together
+#pragma unroll 2
+      for (int j = 0; j < a.q_words / 4; j += 2) {
+        const uint4 v0 = __ldg(q + (size_t)j * kCols), v1 = __ldg(q + (size_t)(j + 1) * kCols);
+        tc_st4(at + 4u * j, v0);
+        tc_st4(at + 4u * j + 4u, v1);
+      }
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.q_full);
     };
-    unsigned i = 0;
+    unsigned i = 0, seg = 0;
     bool go = true, more = w.next(a);
     if (more) load_q(w.unit(a));
-    while (go && more) {
-      const long long u = w.unit(a), len = tree_row_len(a, w.b);
-      const int nodes = a.tree.n_nodes ? a.tree.n_nodes[w.b] : a.n_q;  // (a row that does not fit has no tiles)
-      const long long s0 = len - nodes;
-      const int col = (w.k % a.col_tiles) * kCols + tid;
-      const bool live = col < a.G * a.n_q;
-      const int node = live ? col / a.G : 0;
-      unsigned long long mask = live ? a.tree.mask[(size_t)w.b * a.n_q + node] : 0ull;
-      if (nodes < 64) mask &= (1ull << nodes) - 1ull;
-      const float qs = a.q_scale[(size_t)u * kCols + tid];
-      float m = -INFINITY, l = 0.f;
-      const int n = w.n, lt0 = w.lt0;
-      for (int t = 0; t < n; ++t, ++i) {
-        const unsigned buf = i & 1u, use = i >> 1;
-        if (!__all_sync(0xffffffffu, tree_wait(s, &s.qk_done[buf], use & 1u))) {
-          go = false;
-          break;
-        }
-        tc_fence_after();
-        unsigned x[2][32];
-        tc_ld32(x[0], row + kTmemS + 64u * buf);
-        tc_ld32(x[1], row + kTmemS + 64u * buf + 32u);
-        const float f[2] = {s.scale[i % kMetas][0] * qs, s.scale[i % kMetas][1] * qs};
-        const int valid = s.valid[i % kMetas];
-        const long long t0 = (long long)(lt0 + t) * kTile;
-        tc_wait_ld();
-        if (valid < kTile || t0 + kTile > s0) {  // the same for the whole CTA
-          const long long d = t0 - s0;   // tokens of the tile before the nodes are seen by all
-          unsigned long long vis = d <= -64 ? ~0ull : d < 0 ? ~0ull >> (64 + d) | mask << -d : d < 64 ? mask >> d : 0ull;
-          if (valid < kTile) vis &= (1ull << valid) - 1ull;
-#pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (!(vis >> e & 1ull)) x[e >> 5][e & 31] = 0xff800000u;
-        }
-        float top[2];
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float t1 = __uint_as_float(x[hf][0]), t2 = __uint_as_float(x[hf][1]);
-#pragma unroll
-          for (int e = 2; e < 32; e += 2) {
-            t1 = fmaxf(t1, __uint_as_float(x[hf][e]));
-            t2 = fmaxf(t2, __uint_as_float(x[hf][e + 1]));
-          }
-          top[hf] = fmaxf(t1, t2) * f[hf];
-        }
-        const float mx = fmaxf(top[0], top[1]);
-        // move the reference maximum when some column's tile exceeds it by 2^3
-        if (__any_sync(0xffffffffu, mx > m + 3.f)) {
-          const float mn = fmaxf(m, mx);
-          const float c = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
-          m = mn;
-          l *= c;
-          if (t > 0) {
-            if (!__all_sync(0xffffffffu, tree_wait(s, &s.pv_done[(i - 1) & 1u], ((i - 1) >> 1) & 1u))) {
-              go = false;
-              break;
-            }
-            tc_fence_after();
 #pragma unroll 1
-            for (int o = 0; o < 4; ++o) {
-              unsigned y[32];
-              tc_ld32(y, row + kTmemO + 32u * o);
-              tc_wait_ld();
+    while (go && more) {
+      const long long u = w.unit(a);
+      const int nodes = a.tree.n_nodes ? a.tree.n_nodes[w.b] : a.n_q;  // (a row that does not fit has no tiles)
+      const int col = (w.k % a.col_tiles) * kCols + c;
+      const bool live = col < a.G * a.n_q;
+      unsigned long long mask = live ? a.tree.mask[(size_t)w.b * a.n_q + col / a.G] : 0ull;
+      if (nodes < 64) mask &= (1ull << nodes) - 1ull;
+      const float qs = a.q_scale[(size_t)u * kCols + c];
+      float m = -INFINITY, l = 0.f;
+      const int n = w.n;
+      long long before = tree_row_len(a, w.b) - nodes - (long long)w.lt0 * kTile;  // tokens before the nodes, from the tile on
+#pragma unroll 1
+      for (int t = 0; t < n; ++t, ++i, before -= kTile) {
+        if ((i & 1u) != grp) continue;
+        const unsigned use = i >> 1;
+        if (!wait(&s.qk_done[grp], use & 1u)) {
+          go = false;
+          break;
+        }
+        /*softmax:after_qk*/
+        tc_fence_after();
+        const int valid = s.valid[i % kMetas];
+        const bool masked = valid < kTile || before < kTile;  // the same for the whole CTA
+        // scores of one half of the tile, 32 tokens at a time (read twice: for the maximum and
+        // for the exponentials)
+        unsigned x[32];
+        auto load_half = [&](int h) {
+          tc_ld32(x, row + kTmemS + 64u * grp + 32u * h);
+          tc_wait_ld();
+          if (masked) {
+            // bit e: the column sees token e of the half
+            const int b = int(max(-64LL, min(before - 32 * h, 32LL))), v = valid - 32 * h;
+            unsigned vis = b >= 32 ? ~0u : b > 0 ? ~0u >> (32 - b) | unsigned(mask << b) : b > -64 ? unsigned(mask >> -b) : 0u;
+            if (v < 32) vis &= v > 0 ? (1u << v) - 1u : 0u;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * c);
-              tc_st32(row + kTmemO + 32u * o, y);
-            }
-            tc_wait_st();
+            for (int e = 0; e < 32; ++e)
+              if (!(vis >> e & 1u)) x[e] = 0xff800000u;
+          }
+        };
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          load_half(h);
+          float t1 = __uint_as_float(x[0]), t2 = __uint_as_float(x[1]);
+#pragma unroll
+          for (int e = 2; e < 30; e += 4) {
+            t1 = max3(t1, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+            t2 = max3(t2, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+          }
+          mx = fmaxf(mx, fmaxf(max3(t1, __uint_as_float(x[30]), __uint_as_float(x[31])), t2) * s.scale[i % kMetas][h]);
+        }
+        mx *= qs;
+        /*softmax:after_ld*/
+        if (i > 0 && !wait(&s.max_done[grp ^ 1u][quad], ((i - 1) >> 1) & 1u)) {
+          go = false;
+          break;
+        }
+        // the reference starts 2^5 above the first tile's maximum and moves when some column's
+        // tile exceeds it by 2^3, to 2^5 above that
+        const float mo = t > 0 ? s.mref[c] : -INFINITY;
+        const bool above = mx > mo + 3.f;
+        const bool move = __any_sync(0xffffffffu, above) || t == 0;
+        const float mn = above ? mx + 5.f : mo;
+        if (move) s.mref[c] = mn;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.max_done[grp][quad]);
+        if (move && t > 0) {
+          if (!wait(&s.pv_done[grp ^ 1u], ((i - 1) >> 1) & 1u)) {
+            go = false;
+            break;
+          }
+          tc_fence_after();
+          const float r = mn == -INFINITY ? 1.f : fast_exp2(mo - mn);
+#pragma unroll 1
+          for (int o = 0; o < 8; ++o) {
+            unsigned y[16];
+            tc_ld16(y, row + kTmemO + 16u * o);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * r);
+            tc_st16(row + kTmemO + 16u * o, y);
           }
         }
+        /*softmax:after_max*/
+        if (m != mn) l *= fast_exp2(m - mn);  // (m = -inf: l is 0)
+        m = mn;
         const float mb = m == -INFINITY ? 0.f : m;  // a column that has seen nothing: weights of 0
-        unsigned p[32];
-        float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-        for (int e = 0; e < 64; e += 4) {
-          const float ff = f[e >> 5];
-          const float4 v = *reinterpret_cast<const float4*>(&s.vnorm[i % kMetas][e]);
-          const unsigned* xe = &x[e >> 5][e & 31];
-          const float p0 = fast_exp2(fmaf(__uint_as_float(xe[0]), ff, -mb)), p1 = fast_exp2(fmaf(__uint_as_float(xe[1]), ff, -mb));
-          const float p2 = fast_exp2(fmaf(__uint_as_float(xe[2]), ff, -mb)), p3 = fast_exp2(fmaf(__uint_as_float(xe[3]), ff, -mb));
-          l0 += p0 + p2;
-          l1 += p1 + p3;
-          p[e >> 1] = pack_h2(p0 * v.x, p1 * v.y);
-          p[(e >> 1) + 1] = pack_h2(p2 * v.z, p3 * v.w);
-        }
-        l += l0 + l1;
-        if (use > 0 && !__all_sync(0xffffffffu, tree_wait(s, &s.pv_done[buf], (use - 1) & 1u))) {
+        if (use > 0 && !wait(&s.pv_done[grp], (use - 1) & 1u)) {  // P's buffer
           go = false;
           break;
         }
         tc_fence_after();
-        tc_st32(row + kTmemP + 32u * buf, p);
+        const unsigned long long nm = pack2(-mb, -mb);
+        unsigned long long l2 = 0ull, l3 = 0ull;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          load_half(h);
+          unsigned p[16];
+          const float f = s.scale[i % kMetas][h] * qs;
+          const unsigned long long ff = pack2(f, f);
+          const float4* vn = reinterpret_cast<const float4*>(&s.vnorm[i % kMetas][32 * h]);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 v = vn[e >> 2];
+            const float2 a0 = unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), ff, nm));
+            const float2 a1 = unpack2(fma2(pack2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), ff, nm));
+            const unsigned long long p0 = pack2(fast_exp2(a0.x), fast_exp2(a0.y)), p1 = pack2(fast_exp2(a1.x), fast_exp2(a1.y));
+            l2 = add2(l2, p0);
+            l3 = add2(l3, p1);
+            const float2 w0 = unpack2(mul2(p0, pack2(v.x, v.y))), w1 = unpack2(mul2(p1, pack2(v.z, v.w)));
+            p[e >> 1] = pack_h2(w0.x, w0.y);
+            p[(e >> 1) + 1] = pack_h2(w1.x, w1.y);
+          }
+          tc_st16(row + kTmemP + 32u * grp + 16u * h, p);
+        }
+        const float2 ls = unpack2(add2(l2, l3));
+        l += ls.x + ls.y;
+        /*softmax:after_exp*/
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s.p_full[buf]);
+        if (lane == 0) mbar_arrive(&s.p_full[grp]);
+        /*softmax:after_st*/
       }
       if (!go) break;
-      // the next unit's Q' may come in (this unit's last scores are done), then this unit's
-      // partial goes out
+      // the unit's final reference is the last tile's; its last scores are done then, so the
+      // next unit's Q' may come in. Afterwards this unit's partial goes out, each group
+      // writing half of O's columns.
+      const unsigned last = i - 1;
+      if ((last & 1u) != grp && !wait(&s.max_done[grp ^ 1u][quad], (last >> 1) & 1u)) break;
+      const float mf = s.mref[c];
+      tc_fence_after();
       more = w.next(a);
       if (more) load_q(w.unit(a));
-      const unsigned last = i - 1;
-      if (!__all_sync(0xffffffffu, tree_wait(s, &s.pv_done[last & 1u], (last >> 1) & 1u))) break;
+      if (m != mf) l *= fast_exp2(m - mf);
+      if (grp) {
+        s.total[seg & 1u][c] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.sum_done[quad]);
+      }
+      if (!wait(&s.pv_done[last & 1u], (last >> 1) & 1u)) break;
       tc_fence_after();
       const long long slot = (long long)blockIdx.x + u;
-      float4* po = a.part_o + (size_t)slot * 32 * kCols + tid;
+      float4* po = a.part_o + (size_t)slot * 32 * kCols + c;
 #pragma unroll 1
-      for (int o = 0; o < 4; ++o) {
-        unsigned y[32];
-        tc_ld32(y, row + kTmemO + 32u * o);
+      for (int o = 4 * grp; o < 4 * int(grp) + 4; ++o) {
+        unsigned y[16];
+        tc_ld16(y, row + kTmemO + 16u * o);
         tc_wait_ld();
         if (live)
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            po[(size_t)(8 * o + e) * kCols] = make_float4(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1]),
+          for (int e = 0; e < 4; ++e)
+            po[(size_t)(4 * o + e) * kCols] = make_float4(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1]),
                                                           __uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3]));
       }
       tc_fence_before();
-      if (live) a.part_ml[(size_t)slot * kCols + tid] = make_float2(m, l);
+      if (!grp) {
+        if (!wait(&s.sum_done[quad], seg & 1u)) break;
+        if (live) a.part_ml[(size_t)slot * kCols + c] = make_float2(mf, l + s.total[seg & 1u][c]);
+      }
+      ++seg;
     }
   }
   __syncwarp();
   if (lane == 0 && *reinterpret_cast<volatile int*>(&s.abort)) {
     atomicOr(L.status, BGTQ_STATUS_TIMEOUT);
     // matrix instructions in flight end before tensor memory is freed
-    if (warp == kMmaWarp) {
-      tc_commit(&s.q_full);
+    if (warp == kMmaWarp)
+#pragma unroll 1
       for (unsigned k = 0; k < 4096u; ++k) __nanosleep(256);
-    }
   }
   tc_fence_before();
   __syncthreads();
@@ -637,21 +889,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
   __syncthreads();
 }
 
-// Rows' tile prefix (block 0) and Q' of 32 query columns per block (row, KV head): thread
-// (packed dim p, half) sums R_g[i][j] q[j] for 16 columns from the transposed rotation
-// (coalesced), a power of two per column brings its largest entry near 2^13, then the fp16
-// hi and lo words go out in tensor-memory order. Latency bound.
+// Rows' tile prefix (block 0) and Q' of 32 query columns per block (row, KV head). The key
+// rotations come into shared memory whole, their loads in flight together with the queries;
+// thread (packed dim p, half) then sums R_g[i][j] q[j] for 16 columns, a power of two per
+// column brings its largest entry near 2^13, and the fp16 hi and lo words go out in
+// tensor-memory order. Latency bound: 512 blocks of the 70B-shaped layer with 64 nodes.
 constexpr int kPrepCols = 32;
+constexpr int kColLd = kPrepCols + 4;   // row of 32 columns in shared memory, 16-byte aligned
+constexpr int kPrepSmem = (kD * kD + kD * kColLd) * int(sizeof(float));
 __global__ void __launch_bounds__(256) tree_prep_kernel(DevLayout L, TreeLaunch a, const void* __restrict__ q, int q_dtype,
                                                         float qscale, long long* __restrict__ prefix,
                                                         unsigned* __restrict__ qt, float* __restrict__ q_scale) {
-  __shared__ __align__(16) float s_q[kPrepCols][kD], s_r[kPrepCols][kD + 1];
+  extern __shared__ __align__(128) unsigned char smem[];
+  float* s_rot = reinterpret_cast<float*>(smem);      // the groups' rotations, transposed, one after the other
+  float* s_q = s_rot + kD * kD;                       // [packed dim][column], then q' likewise
   __shared__ float s_up[kPrepCols];
   __shared__ short s_pc[kD], s_dim[kMaxDims];
   pdl_trigger();
   const int tid = threadIdx.x, N = a.G * a.n_q, blocks = a.col_tiles * (kCols / kPrepCols);
   if (blockIdx.x == 0 && tid < 32) {
     long long run = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
       const int b = b0 + tid;
       long long v = 0;
@@ -676,10 +934,25 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(DevLayout L, TreeLaunch 
   const int c0 = cb * kPrepCols;
   const long long u = (long long)b * a.row_units + (long long)h * a.col_tiles + c0 / kCols;
   const int in0 = c0 % kCols;  // first column inside the unit
+  const int qw = a.q_words;
+  if (c0 >= N) {  // columns that no query has: zeros
+    for (int e = tid; e < kPrepCols * 2 * qw / 4; e += 256)
+      reinterpret_cast<uint4*>(qt)[((size_t)u * (2 * qw / 4) + e / kPrepCols) * kCols + in0 + e % kPrepCols] = make_uint4(0, 0, 0, 0);
+    if (tid < kPrepCols) q_scale[(size_t)u * kCols + in0 + tid] = 1.f;
+    return;
+  }
+  for (int g = 0, at = 0; g < L.n_kgroups; ++g) {
+    const int n = L.group_dim[g] * L.group_dim[g];  // (dimensions are even: a multiple of 4)
+    const float4* src = reinterpret_cast<const float4*>(L.k_rot32t[g]);
+#pragma unroll 4
+    for (int e = tid; e < n / 4; e += 256) reinterpret_cast<float4*>(s_rot + at)[e] = __ldg(src + e);
+    at += n;
+  }
   if (tid < kD) s_pc[tid] = L.packed_coord[tid];
   // packed dim of every operand dim (quads of 8; -1 where a quad has no pair)
   for (int e = tid; e < 8 * L.n_kquads; e += 256) s_dim[e] = (e & 7) < 2 * L.quad_np[e >> 3] ? short(L.quad_dim0[e >> 3] + (e & 7)) : short(-1);
   __syncthreads();
+#pragma unroll 8
   for (int e = tid; e < kPrepCols * kD; e += 256) {
     const int c = e >> 7, p = e & (kD - 1), col = c0 + c;
     float x = 0.f;
@@ -687,74 +960,95 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(DevLayout L, TreeLaunch 
       const size_t r = ((size_t)b * a.n_q + col / a.G) * (a.G * a.h_kv) + (size_t)h * a.G + col % a.G;
       x = load_q(q, q_dtype, r * kD + s_pc[p]);
     }
-    s_q[c][p] = x;
+    s_q[p * kColLd + c] = x;
   }
   __syncthreads();
-  {
-    const int p = tid & (kD - 1), half = tid >> 7;
-    float acc[16];
+  const int p = tid & (kD - 1), half = tid >> 7;
+  float acc[16];
 #pragma unroll
-    for (int c = 0; c < 16; ++c) acc[c] = 0.f;
-    float f = 0.f;
-    if (p < L.n_packed) {
-      int g = 0;
-      while (g + 1 < L.n_kgroups && p >= L.group_off[g + 1]) ++g;
-      const int d = L.group_dim[g], off = L.group_off[g];
-      const float* R = L.k_rot32t[g] + (p - off);
-      f = qscale * rsqrtf(float(d)) * L.inv_kappa_group[g];
+  for (int c = 0; c < 16; ++c) acc[c] = 0.f;
+  float f = 0.f;
+  if (p < L.n_packed) {
+    int g = 0, at = 0;
+    while (g + 1 < L.n_kgroups && p >= L.group_off[g + 1]) {
+      at += L.group_dim[g] * L.group_dim[g];
+      ++g;
+    }
+    const int d = L.group_dim[g], off = L.group_off[g];
+    const float* R = s_rot + at + (p - off);
+    const float* x = s_q + off * kColLd + 16 * half;
+    f = qscale * rsqrtf(float(d)) * L.inv_kappa_group[g];
 #pragma unroll 4
-      for (int j = 0; j < d; ++j) {
-        const float r = __ldg(R + (size_t)j * d);
+    for (int j = 0; j < d; ++j) {
+      const float r = R[j * d];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) acc[c] = fmaf(r, s_q[16 * half + c][off + j], acc[c]);
+      for (int k = 0; k < 4; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(x + j * kColLd + 4 * k);
+        acc[4 * k] = fmaf(r, v.x, acc[4 * k]);
+        acc[4 * k + 1] = fmaf(r, v.y, acc[4 * k + 1]);
+        acc[4 * k + 2] = fmaf(r, v.z, acc[4 * k + 2]);
+        acc[4 * k + 3] = fmaf(r, v.w, acc[4 * k + 3]);
       }
     }
-#pragma unroll
-    for (int c = 0; c < 16; ++c) s_r[16 * half + c][p] = acc[c] * f;
   }
   __syncthreads();
-  {
-    const int lane = tid & 31, warp = tid >> 5;
-    for (int c = warp; c < kPrepCols; c += 8) {
-      float top = 0.f;
-      for (int p = lane; p < kD; p += 32) {
-        const float x = fabsf(s_r[c][p]);
-        if (x <= 3.0e38f) top = fmaxf(top, x);
-      }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (lane == 0) {
-        const int ex = top > 0.f ? min(100, max(-100, 13 - (int(__float_as_uint(top) >> 23) - 127))) : 0;
-        s_up[c] = __int_as_float((127 + ex) << 23);
-        q_scale[(size_t)u * kCols + in0 + c] = __int_as_float((127 - ex) << 23);
-      }
+  for (int k = 0; k < 4; ++k)
+    *reinterpret_cast<float4*>(s_q + p * kColLd + 16 * half + 4 * k) =
+        make_float4(acc[4 * k] * f, acc[4 * k + 1] * f, acc[4 * k + 2] * f, acc[4 * k + 3] * f);
+  __syncthreads();
+  if (tid < 8 * kPrepCols) {  // eight threads per column
+    const int c = tid >> 3;
+    float top = 0.f;
+    for (int e = tid & 7; e < kD; e += 8) {
+      const float x = fabsf(s_q[e * kColLd + c]);
+      if (x <= 3.0e38f) top = fmaxf(top, x);  // (an infinite or NaN q' keeps its column so)
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if ((tid & 7) == 0) {
+      const int ex = top > 0.f ? min(100, max(-100, 13 - (int(__float_as_uint(top) >> 23) - 127))) : 0;
+      s_up[c] = __int_as_float((127 + ex) << 23);
+      q_scale[(size_t)u * kCols + in0 + c] = __int_as_float((127 - ex) << 23);
     }
   }
   __syncthreads();
   // word w of a column's part = operand dims 2w, 2w + 1; groups of 4 words, columns innermost
-  const int qw = a.q_words;
-  for (int e = tid; e < kPrepCols * qw; e += 256) {
-    const int k = e & 3, c = (e >> 2) % kPrepCols, w = (e >> 2) / kPrepCols * 4 + k;
-    float v[2];
+  for (int e = tid; e < kPrepCols * qw / 4; e += 256) {
+    const int c = e % kPrepCols, w = e / kPrepCols;
+    unsigned hi[4], lo[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int dim = 2 * w + i < 8 * L.n_kquads ? s_dim[2 * w + i] : -1;
-      v[i] = dim >= 0 ? s_r[c][dim] * s_up[c] : 0.f;
+    for (int k = 0; k < 4; ++k) {
+      float v[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int od = 8 * w + 2 * k + i, dim = od < 8 * L.n_kquads ? s_dim[od] : -1;
+        v[i] = dim >= 0 ? s_q[dim * kColLd + c] * s_up[c] : 0.f;
+      }
+      const float h0 = __half2float(__float2half_rn(v[0])), h1 = __half2float(__float2half_rn(v[1]));
+      hi[k] = pack_h2(h0, h1);
+      lo[k] = pack_h2(v[0] - h0, v[1] - h1);
     }
-    const float h0 = __half2float(__float2half_rn(v[0])), h1 = __half2float(__float2half_rn(v[1]));
-    const size_t at = ((size_t)u * (2 * qw / 4) + w / 4) * kCols * 4 + (in0 + c) * 4 + k;
-    qt[at] = pack_h2(h0, h1);
-    qt[at + (size_t)(qw / 4) * kCols * 4] = pack_h2(v[0] - h0, v[1] - h1);
+    uint4* at = reinterpret_cast<uint4*>(qt) + ((size_t)u * (2 * qw / 4) + w) * kCols + in0 + c;
+    at[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    at[(size_t)(qw / 4) * kCols] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
 }
 
-// Merge of a unit's partials for 32 query columns per block, then out = R_V^T o' / l:
-// thread (output dim, half) sums 16 columns, the rotation read from L2 once per block.
+// Merge of a unit's partials for 32 query columns per block, then out = R_V^T o' / l with the
+// rotation in shared memory (fetched before the wait for the partials): thread (output dim,
+// half) sums 16 columns. Bound by its shared-memory reads and by latency.
+constexpr int kCombSmem = (kD * kD + kD * kColLd) * int(sizeof(float));
 __global__ void __launch_bounds__(256) tree_combine_kernel(DevLayout L, TreeLaunch a, int n_ctas, void* __restrict__ out,
                                                            int out_dtype) {
-  __shared__ __align__(16) float s_o[kPrepCols][kD];
-  const int tid = threadIdx.x, N = a.G * a.n_q, blocks = a.col_tiles * (kCols / kPrepCols);
+  extern __shared__ __align__(128) unsigned char smem[];
+  float* s_rot = reinterpret_cast<float*>(smem);   // R_V [i][d]
+  float* s_o = s_rot + kD * kD;                    // [value dim][column]
+  const int tid = threadIdx.x, N = a.G * a.n_q, blocks = (N + kPrepCols - 1) / kPrepCols;
   pdl_trigger();
+#pragma unroll
+  for (int e = 0; e < kD * kD / 4 / 256; ++e)
+    reinterpret_cast<float4*>(s_rot)[e * 256 + tid] = __ldg(reinterpret_cast<const float4*>(L.v_rot32) + e * 256 + tid);
   pdl_wait();
   const int cb = blockIdx.x % blocks, bh = blockIdx.x / blocks, h = bh % a.h_kv, b = bh / a.h_kv;
   const int c0 = cb * kPrepCols, in0 = c0 % kCols;
@@ -763,31 +1057,52 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(DevLayout L, TreeLaun
   const long long T = a.prefix[a.batch], C = min((long long)n_ctas, T), p0 = a.prefix[b], nt = (a.prefix[b + 1] - p0) / a.row_units;
   const int c = tid & 31, wp = tid >> 5;  // merge: column c, float4s wp, wp + 8, ..
   // (a row without tiles has no partials: zeros)
-  int first = 0, last = -1;
+  int first = 0, n = 0;
   if (nt > 0) {
     first = cta_of_tile(p0 + k * nt, T, C);
-    last = cta_of_tile(p0 + (k + 1) * nt - 1, T, C);
+    n = cta_of_tile(p0 + (k + 1) * nt - 1, T, C) + 1 - first;
   }
-  float top = -INFINITY;
   const bool live = c0 + c < N;
-  if (live)
-    for (int ct = first; ct <= last; ++ct) top = fmaxf(top, a.part_ml[(size_t)(ct + u) * kCols + in0 + c].x);
-  float l = 0.f;
+  const float2* ml = a.part_ml + (size_t)(first + u) * kCols + in0 + c;
+  const float4* po = a.part_o + ((size_t)(first + u) * 32 + wp) * kCols + in0 + c;
+  float top = -INFINITY, l = 0.f;
   float4 o[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (live && top != -INFINITY)
-    for (int ct = first; ct <= last; ++ct) {
-      const float2 ml = a.part_ml[(size_t)(ct + u) * kCols + in0 + c];
-      if (ml.x == -INFINITY) continue;
-      const float f = exp2f(ml.x - top);
-      l = fmaf(f, ml.y, l);
+  // kSlots partials at a time, their loads in flight together; the running maximum as usual
+  constexpr int kSlots = 4;
+#pragma unroll 1
+  for (int s0 = 0; live && s0 < n; s0 += kSlots) {
+    float2 v[kSlots];
+    float4 x[kSlots][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 x = __ldcs(a.part_o + ((size_t)(ct + u) * 32 + wp + 8 * j) * kCols + in0 + c);
-        o[j] = make_float4(fmaf(f, x.x, o[j].x), fmaf(f, x.y, o[j].y), fmaf(f, x.z, o[j].z), fmaf(f, x.w, o[j].w));
-      }
+    for (int i = 0; i < kSlots; ++i) {
+      const int sl = min(s0 + i, n - 1);
+      v[i] = ml[(size_t)sl * kCols];
+      if (s0 + i >= n) v[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[i][j] = __ldcs(po + ((size_t)sl * 32 + 8 * j) * kCols);
     }
+    float m = top;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) m = fmaxf(m, v[i].x);
+    if (m == -INFINITY) continue;
+    const float r = exp2f(top - m);
+    l *= r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = make_float4(o[j].x * r, o[j].y * r, o[j].z * r, o[j].w * r);
+    top = m;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      if (v[i].x == -INFINITY) continue;
+      const float f = exp2f(v[i].x - m);
+      l = fmaf(f, v[i].y, l);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o[j] = make_float4(fmaf(f, x[i][j].x, o[j].x), fmaf(f, x[i][j].y, o[j].y), fmaf(f, x[i][j].z, o[j].z),
+                           fmaf(f, x[i][j].w, o[j].w));
+    }
+  }
   const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -795,24 +1110,24 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(DevLayout L, TreeLaun
     const float x[4] = {o[j].x, o[j].y, o[j].z, o[j].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int n = 4 * (wp + 8 * j) + e;
-      s_o[c][16 * (n & 7) + (n >> 3)] = x[e] * inv;
+      const int nn = 4 * (wp + 8 * j) + e;
+      s_o[(16 * (nn & 7) + (nn >> 3)) * kColLd + c] = x[e] * inv;
     }
   }
   __syncthreads();
   const int d = tid & (kD - 1), half = tid >> 7;
-  float acc[16];
+  unsigned long long acc[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-#pragma unroll 2
-  for (int i = 0; i < kD; i += 4) {
-    float r[4];
+  for (int i = 0; i < 8; ++i) acc[i] = 0ull;
+#pragma unroll 8
+  for (int i = 0; i < kD; ++i) {
+    const float r = s_rot[i * kD + d];
+    const unsigned long long rr = pack2(r, r);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = __ldg(L.v_rot32 + (size_t)(i + e) * kD + d);
-#pragma unroll
-    for (int cc = 0; cc < 16; ++cc) {
-      const float4 x = *reinterpret_cast<const float4*>(&s_o[16 * half + cc][i]);
-      acc[cc] = fmaf(r[0], x.x, fmaf(r[1], x.y, fmaf(r[2], x.z, fmaf(r[3], x.w, acc[cc]))));
+    for (int e = 0; e < 4; ++e) {
+      const float4 x = *reinterpret_cast<const float4*>(s_o + i * kColLd + 16 * half + 4 * e);
+      acc[2 * e] = fma2(rr, pack2(x.x, x.y), acc[2 * e]);
+      acc[2 * e + 1] = fma2(rr, pack2(x.z, x.w), acc[2 * e + 1]);
     }
   }
 #pragma unroll
@@ -820,7 +1135,9 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(DevLayout L, TreeLaun
     const int col = c0 + 16 * half + cc, node = col / a.G;
     // rows past a row's drafted nodes are not written (a row that does not fit: zeros)
     if (col >= N || (n_nodes >= 0 && node >= n_nodes)) continue;
-    store_out(out, out_dtype, (((size_t)b * a.n_q + node) * (a.G * a.h_kv) + (size_t)h * a.G + col % a.G) * kD + d, acc[cc]);
+    const float2 y = unpack2(acc[cc >> 1]);
+    store_out(out, out_dtype, (((size_t)b * a.n_q + node) * (a.G * a.h_kv) + (size_t)h * a.G + col % a.G) * kD + d,
+              cc & 1 ? y.y : y.x);
   }
 }
 
@@ -828,27 +1145,32 @@ int tree_q_words(const DevLayout& L) { return (L.n_kquads + 1) / 2 * 8; }
 
 int tree_smem_bytes(const DevLayout& L, int stages) {
   const int vt = L.v_rate == 3 ? vtab_bytes<3>() : L.v_rate == 4 ? vtab_bytes<4>() : 0;
-  return kTbl8Bytes + kTbl3Bytes + vt + 128 + 4 * ((L.n_kquads + 1) / 2) * 2048 + 2 * 16384 +
+  return kTbl8Bytes + kTbl3Bytes + vt + 128 + kUnitBytes + 4 * ((L.n_kquads + 1) / 2) * 2048 + 2 * 16384 +
          stages * (kNormBytes + L.tile_bytes);
+}
+
+// Once per device: the kernel's dynamic shared memory limit raised to what a block may use.
+template <typename K>
+cudaError_t raise_smem_limit(K kernel, bool (&done)[64]) {
+  int dev = 0, optin = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  if (done[dev]) return cudaSuccess;
+  cudaFuncAttributes fa{};
+  e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kernel);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - int(fa.sharedSizeBytes));
+  done[dev] = e == cudaSuccess;
+  return e;
 }
 
 template <int VR, bool NH>
 cudaError_t launch_tree_kernel(const DevLayout& L, const TreeLaunch& a, unsigned grid, int smem, cudaStream_t stream) {
   static bool done[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = raise_smem_limit(tree_kernel<VR, NH>, done);
   if (e != cudaSuccess) return e;
-  if (dev >= 64) return cudaErrorInvalidDevice;
-  if (!done[dev]) {
-    int optin = 0;
-    cudaFuncAttributes fa{};
-    e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, tree_kernel<VR, NH>);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(tree_kernel<VR, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - int(fa.sharedSizeBytes));
-    if (e != cudaSuccess) return e;
-    done[dev] = true;
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kTreeThreads);
@@ -915,11 +1237,15 @@ cudaError_t launch_tree(const DevLayout& L, const TreePlan& plan, const void* q,
   const int smem = tree_smem_bytes(L, a.stages);
   if (smem > limit) return cudaErrorInvalidValue;
   const unsigned blocks = unsigned((long long)batch * h_kv * plan.col_tiles * (kCols / kPrepCols));
-  tree_prep_kernel<<<blocks, 256, 0, stream>>>(L, a, q, q_dtype, softmax_scale * kLog2e,
+  static bool prep_done[64] = {}, comb_done[64] = {};
+  cudaError_t e = raise_smem_limit(tree_prep_kernel, prep_done);
+  if (e == cudaSuccess) e = raise_smem_limit(tree_combine_kernel, comb_done);
+  if (e != cudaSuccess) return e;
+  tree_prep_kernel<<<blocks, 256, kPrepSmem, stream>>>(L, a, q, q_dtype, softmax_scale * kLog2e,
                                                reinterpret_cast<long long*>(ws + plan.prefix_at),
                                                reinterpret_cast<unsigned*>(ws + plan.q_at),
                                                reinterpret_cast<float*>(ws + plan.scale_at));
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const unsigned grid = unsigned(plan.n_ctas);
   auto go = [&](auto vr) {
@@ -934,7 +1260,17 @@ cudaError_t launch_tree(const DevLayout& L, const TreePlan& plan, const void* q,
     default: e = go(IntC<4>{}); break;
   }
   if (e != cudaSuccess) return e;
-  return launch_dependent(tree_combine_kernel, blocks, 256, stream, L, a, plan.n_ctas, out, out_dtype);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((long long)batch * h_kv * ((a.G * n_q + kPrepCols - 1) / kPrepCols)));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = kCombSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_combine_kernel, L, a, plan.n_ctas, out, out_dtype);
 }
 
 }  // namespace bgtq
