@@ -28,23 +28,53 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kMoveThreads = 256;
-constexpr int kMoveSlots = 8;  // source tiles a CTA holds at a time
+constexpr int kCommitThreads = 256, kGatherThreads = 128;
+constexpr int kMoveSlots = 5;  // source tiles a CTA holds at a time
 
-// Destination string `lane` of key quad Q (rate R): ors in the fields of the destination
-// tokens whose source is present. info[t]: source tile's byte offset from `src` + source
-// token (offsets are multiples of 64), or -1.
-template <int R>
-__device__ __forceinline__ void key_string(uint8_t* dst, const uint8_t* src, const int* info, int P, int lane) {
+// Where the codes of the 64 destination tokens come from, as each part of a tile needs it (byte
+// offsets count from the source tiles' start; a token without a source points at a tile of
+// zeros, so nothing branches on it):
+//  raw: offset of the source tile, row (token % 8) | slot (token / 8) << 8;
+//  key[r - 1]: offset of the row's strings in a full quad of rate r, shift of the slot's field
+//    (rate 3: | 8 row << 8 for the second plane; rate 4: the byte is in the offset);
+//  value: offset of the token's string in its chunk (lane row / 2 of the first four), shift of
+//    its half and parity;
+//  norm: offset of its entry in the first row of norms.
+struct Moves {
+  int2 raw[64], key[4][64], value[64];
+  int norm[64];
+};
+__device__ __forceinline__ void set_move(const DevLayout& L, Moves& mv, int t, int off, int tok) {
+  const int g = tok & 7, m = tok >> 3, hs = m & 1, ps = g & 1, b = L.v_rate;
+  mv.raw[t] = make_int2(off, g | m << 8);
+  mv.key[0][t] = make_int2(off + 8 * g, m);
+  mv.key[1][t] = make_int2(off + 16 * g, 4 * m);
+  mv.key[2][t] = make_int2(off + 16 * g, 6 * m | (8 * g) << 8);
+  mv.key[3][t] = make_int2(off + 32 * g + m, 0);
+  const int lane = g >> 1;
+  mv.value[t] = make_int2(off + L.vcode_off + (m >> 1) * 256 * b + (b == 1 ? 8 : 16) * lane,
+                          (b == 1 ? 16 * ps + 2 * hs : 4 * b * hs + b * ps) | (b == 3 ? 8 : 16) * lane << 8);
+  mv.norm[t] = off + L.knorm_off + (L.norm_fp16 ? 2 : 4) * (g * 8 + m);
+}
+
+// ADD: ors into what was put before, else stores.
+template <bool ADD, typename T>
+__device__ __forceinline__ void put(T* p, T v) {
+  if constexpr (ADD) *p |= v;
+  else *p = v;
+}
+
+// Destination string `lane` of a key quad with P < 4 pairs (rate R): its 8 tokens' fields.
+template <int R, bool ADD>
+__device__ __forceinline__ void key_string(uint8_t* dst, const uint8_t* src, const int2* raw, int P, int lane) {
   if (lane >= 8 * P) return;
   const int g = lane / P, e = lane - g * P;
   unsigned long long D = 0;
 #pragma unroll
   for (int m = 0; m < 8; ++m) {
-    const int x = info[g + 8 * m];
-    if (x < 0) continue;
-    const int tok = x & 63, li = (tok & 7) * P + e, mm = tok >> 3;
-    const uint8_t* s = src + (x - tok);
+    const int2 x = raw[g + 8 * m];
+    const int li = (x.y & 7) * P + e, mm = x.y >> 8;
+    const uint8_t* s = src + x.x;
     if constexpr (R == 1) {
       const unsigned w = *reinterpret_cast<const unsigned short*>(s + 2 * li);
       D |= ((w >> mm) & 0x0101u) << m;
@@ -61,36 +91,76 @@ __device__ __forceinline__ void key_string(uint8_t* dst, const uint8_t* src, con
     }
   }
   if constexpr (R == 1) {
-    *reinterpret_cast<unsigned short*>(dst + 2 * lane) |= static_cast<unsigned short>(D);
+    put<ADD>(reinterpret_cast<unsigned short*>(dst + 2 * lane), static_cast<unsigned short>(D));
   } else if constexpr (R == 2) {
-    *reinterpret_cast<unsigned*>(dst + 4 * lane) |= static_cast<unsigned>(D);
+    put<ADD>(reinterpret_cast<unsigned*>(dst + 4 * lane), static_cast<unsigned>(D));
   } else if constexpr (R == 3) {
-    *reinterpret_cast<unsigned*>(dst + 4 * lane) |= static_cast<unsigned>(D);
-    *reinterpret_cast<unsigned short*>(dst + 32 * P + 2 * lane) |= static_cast<unsigned short>(D >> 32);
+    put<ADD>(reinterpret_cast<unsigned*>(dst + 4 * lane), static_cast<unsigned>(D));
+    put<ADD>(reinterpret_cast<unsigned short*>(dst + 32 * P + 2 * lane), static_cast<unsigned short>(D >> 32));
   } else {
-    *reinterpret_cast<unsigned long long*>(dst + 8 * lane) |= D;
+    put<ADD>(reinterpret_cast<unsigned long long*>(dst + 8 * lane), D);
   }
 }
 
-// Words of value string `lane` of a chunk block (rates 3-4: two planes).
+// The same for a full quad (lane = 4 row + pair): one or two loads, a shift and a mask per token.
+template <int R, bool ADD>
+__device__ __forceinline__ void full_key_string(uint8_t* dst, const uint8_t* src, const int2* key, int lane) {
+  const int g = lane >> 2, e = lane & 3;
+  unsigned D = 0, D1 = 0;
+#pragma unroll
+  for (int m = 0; m < 8; ++m) {
+    const int2 x = key[g + 8 * m];
+    const uint8_t* s = src + x.x;
+    if constexpr (R == 1) {
+      const unsigned w = *reinterpret_cast<const unsigned short*>(s + 2 * e);
+      D |= ((w >> x.y) & 0x0101u) << m;
+    } else if constexpr (R == 2) {
+      const unsigned w = *reinterpret_cast<const unsigned*>(s + 4 * e);
+      D |= ((w >> x.y) & 0xFu) << (4 * m);
+    } else if constexpr (R == 3) {
+      const unsigned lo = *reinterpret_cast<const unsigned*>(s + 4 * e);
+      const unsigned hi = *reinterpret_cast<const unsigned short*>(s + 128 - (x.y >> 8) + 2 * e);
+      const int sh = x.y & 0xff;
+      const unsigned f = (sh < 32 ? __funnelshift_r(lo, hi, sh) : hi >> (sh - 32)) & 0x3Fu;
+      if (6 * m < 32) D |= f << (6 * m);
+      if (6 * m + 6 > 32) D1 |= 6 * m >= 32 ? f << (6 * m - 32) : f >> (32 - 6 * m);
+    } else {
+      const unsigned f = s[8 * e];
+      if (m < 4) D |= f << (8 * m);
+      else D1 |= f << (8 * m - 32);
+    }
+  }
+  if constexpr (R == 1) {
+    put<ADD>(reinterpret_cast<unsigned short*>(dst + 2 * lane), static_cast<unsigned short>(D));
+  } else if constexpr (R == 2) {
+    put<ADD>(reinterpret_cast<unsigned*>(dst + 4 * lane), D);
+  } else if constexpr (R == 3) {
+    put<ADD>(reinterpret_cast<unsigned*>(dst + 4 * lane), D);
+    put<ADD>(reinterpret_cast<unsigned short*>(dst + 128 + 2 * lane), static_cast<unsigned short>(D1));
+  } else {
+    put<ADD>(reinterpret_cast<unsigned long long*>(dst + 8 * lane), D | static_cast<unsigned long long>(D1) << 32);
+  }
+}
+
+// Words of a value string at s (rates 3-4: the second plane's words at s2).
 template <int VR>
-__device__ __forceinline__ void load_value_string(const uint8_t* blk, int lane, unsigned (&w)[2 * VR]) {
+__device__ __forceinline__ void load_value_string(const uint8_t* s, const uint8_t* s2, unsigned (&w)[2 * VR]) {
   if constexpr (VR == 1) {
-    const uint2 x = *reinterpret_cast<const uint2*>(blk + 8 * lane);
+    const uint2 x = *reinterpret_cast<const uint2*>(s);
     w[0] = x.x;
     w[1] = x.y;
   } else {
-    const uint4 x = *reinterpret_cast<const uint4*>(blk + 16 * lane);
+    const uint4 x = *reinterpret_cast<const uint4*>(s);
     w[0] = x.x;
     w[1] = x.y;
     w[2] = x.z;
     w[3] = x.w;
     if constexpr (VR == 3) {
-      const uint2 y = *reinterpret_cast<const uint2*>(blk + 512 + 8 * lane);
+      const uint2 y = *reinterpret_cast<const uint2*>(s2);
       w[4] = y.x;
       w[5] = y.y;
     } else if constexpr (VR == 4) {
-      const uint4 y = *reinterpret_cast<const uint4*>(blk + 512 + 16 * lane);
+      const uint4 y = *reinterpret_cast<const uint4*>(s2);
       w[4] = y.x;
       w[5] = y.y;
       w[6] = y.z;
@@ -99,99 +169,132 @@ __device__ __forceinline__ void load_value_string(const uint8_t* blk, int lane, 
   }
 }
 template <int VR>
-__device__ __forceinline__ void store_value_string(uint8_t* blk, int lane, const unsigned (&w)[2 * VR]) {
+__device__ __forceinline__ void store_value_string(uint8_t* s, uint8_t* s2, const unsigned (&w)[2 * VR]) {
   if constexpr (VR == 1) {
-    *reinterpret_cast<uint2*>(blk + 8 * lane) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(s) = make_uint2(w[0], w[1]);
   } else {
-    *reinterpret_cast<uint4*>(blk + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
-    if constexpr (VR == 3) *reinterpret_cast<uint2*>(blk + 512 + 8 * lane) = make_uint2(w[4], w[5]);
-    else if constexpr (VR == 4) *reinterpret_cast<uint4*>(blk + 512 + 16 * lane) = make_uint4(w[4], w[5], w[6], w[7]);
+    *reinterpret_cast<uint4*>(s) = make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (VR == 3) *reinterpret_cast<uint2*>(s2) = make_uint2(w[4], w[5]);
+    else if constexpr (VR == 4) *reinterpret_cast<uint4*>(s2) = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 
 // Destination string `lane` of value chunk c: tokens 2 t + 8 h + par of the chunk (h, par in
 // 0..1), every one's codes of the lane's 16 dims taken from string 4 g + t' of its source
-// chunk. dst, src: the tiles' value areas.
-template <int VR>
-__device__ __forceinline__ void value_string(uint8_t* dst, const uint8_t* src, const int* info, int c, int lane) {
+// chunk. dst: the tile's value area; src: the source tiles.
+template <int VR, bool ADD>
+__device__ __forceinline__ void value_string(uint8_t* dst, const uint8_t* src, const int2* value, int c, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  uint8_t* blk = dst + c * 256 * VR;
+  // bytes per string in each plane
+  constexpr int B1 = VR == 1 ? 8 : 16, B2 = VR == 3 ? 8 : 16;
+  uint8_t* d1 = dst + c * 256 * VR + B1 * lane;
+  uint8_t* d2 = dst + c * 256 * VR + 512 + B2 * lane;
   unsigned D[2 * VR];
-  load_value_string<VR>(blk, lane, D);
+  if constexpr (ADD) {
+    load_value_string<VR>(d1, d2, D);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2 * VR; ++i) D[i] = 0u;
+  }
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int h = q >> 1, par = q & 1;
-    const int x = info[16 * c + 2 * t + 8 * h + par];
-    if (x < 0) continue;
-    const int tok = x & 63, jj = tok & 15, hs = jj >> 3, ps = jj & 1;
+    const int2 x = value[16 * c + 2 * t + 8 * h + par];
+    const int sh = x.y & 0xff, l2 = x.y >> 8;   // l2: the second plane's offset of the lane (row / 2)
+    const uint8_t* s = src + x.x + 4 * B1 * g;
     unsigned w[2 * VR];
-    load_value_string<VR>(src + (x - tok) + (tok >> 4) * 256 * VR, 4 * g + ((jj & 7) >> 1), w);
+    load_value_string<VR>(s, VR >= 3 ? src + (x.x - B1 * (l2 / B2)) + 512 + l2 + 4 * B2 * g : s, w);
     if constexpr (VR == 1) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) D[u] |= ((w[u] >> (16 * ps + 2 * hs)) & 0x3333u) << (16 * par + 2 * h);
+      for (int u = 0; u < 2; ++u) D[u] |= ((w[u] >> sh) & 0x3333u) << (16 * par + 2 * h);
     } else if constexpr (VR == 2) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) D[u] |= ((w[u] >> (8 * hs + 2 * ps)) & 0x00330033u) << (8 * h + 2 * par);
+      for (int u = 0; u < 4; ++u) D[u] |= ((w[u] >> sh) & 0x00330033u) << (8 * h + 2 * par);
     } else if constexpr (VR == 3) {
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt) {
-        const int wi = 24 * mt >> 5, sh = 24 * mt & 31;
-        const unsigned grp = sh <= 8 ? w[wi] >> sh : __funnelshift_r(w[wi], w[wi + 1], sh);
-        const unsigned v = ((grp >> (12 * hs + 3 * ps)) & 0x1C7u) << (12 * h + 3 * par);
-        D[wi] |= v << sh;
-        if (sh > 8) D[wi + 1] |= v >> (32 - sh);
+        const int wi = 24 * mt >> 5, b0 = 24 * mt & 31;
+        const unsigned grp = b0 <= 8 ? w[wi] >> b0 : __funnelshift_r(w[wi], w[wi + 1], b0);
+        const unsigned v = ((grp >> sh) & 0x1C7u) << (12 * h + 3 * par);
+        D[wi] |= v << b0;
+        if (b0 > 8) D[wi + 1] |= v >> (32 - b0);
       }
     } else {
 #pragma unroll
-      for (int u = 0; u < 8; ++u) D[u] |= ((w[u] >> (16 * hs + 4 * ps)) & 0x0F0Fu) << (16 * h + 4 * par);
+      for (int u = 0; u < 8; ++u) D[u] |= ((w[u] >> sh) & 0x0F0Fu) << (16 * h + 4 * par);
     }
   }
-  store_value_string<VR>(blk, lane, D);
+  store_value_string<VR>(d1, d2, D);
 }
 
-// Ors the tokens that info names into the tile at dst (zero where nothing was put yet).
-// Warps take key quads and value chunks in turn; the norms follow.
-__device__ __forceinline__ void assemble_tile(const DevLayout& L, uint8_t* dst, const uint8_t* src, const int* info) {
+// The layout's quads as a kernel parameter: byte offset | pairs << 20 | rate << 24.
+struct QuadList {
+  unsigned q[kMaxQuads];
+};
+QuadList quad_list(const DevLayout& L) {
+  QuadList l{};
+  for (int g = 0; g < L.n_kgroups; ++g)
+    for (int i = 0; i < L.group_nquads[g]; ++i) {
+      const int it = L.group_quad0[g] + i;
+      l.q[it] = unsigned(L.quad_off[it]) | unsigned(L.quad_np[it]) << 20 | unsigned(L.group_rate[g]) << 24;
+    }
+  return l;
+}
+
+// Puts the tokens that mv names into the tile at dst (ADD: next to those put there before).
+// NT threads: warps take key quads and value chunks in turn; the norms follow.
+template <int NT, bool ADD>
+__device__ __forceinline__ void assemble_tile(const DevLayout& L, const QuadList& ql, uint8_t* dst, const uint8_t* src,
+                                              const Moves& mv) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nq = L.n_kquads;
-  for (int it = warp; it < nq + 4; it += kMoveThreads / 32) {
+#pragma unroll 1
+  for (int it = warp; it < nq + 4; it += NT / 32) {
     if (it < nq) {
-      int g = 0;
-      while (g + 1 < L.n_kgroups && it >= L.group_quad0[g + 1]) ++g;
-      const int off = L.quad_off[it], P = L.quad_np[it];
-      switch (L.group_rate[g]) {
-        case 1: key_string<1>(dst + off, src + off, info, P, lane); break;
-        case 2: key_string<2>(dst + off, src + off, info, P, lane); break;
-        case 3: key_string<3>(dst + off, src + off, info, P, lane); break;
-        default: key_string<4>(dst + off, src + off, info, P, lane); break;
+      const unsigned q = ql.q[it];
+      const int off = q & 0xfffffu, P = q >> 20 & 15u;
+      if (P == 4) {
+        switch (q >> 24) {
+          case 1: full_key_string<1, ADD>(dst + off, src + off, mv.key[0], lane); break;
+          case 2: full_key_string<2, ADD>(dst + off, src + off, mv.key[1], lane); break;
+          case 3: full_key_string<3, ADD>(dst + off, src + off, mv.key[2], lane); break;
+          default: full_key_string<4, ADD>(dst + off, src + off, mv.key[3], lane); break;
+        }
+      } else {
+        switch (q >> 24) {
+          case 1: key_string<1, ADD>(dst + off, src + off, mv.raw, P, lane); break;
+          case 2: key_string<2, ADD>(dst + off, src + off, mv.raw, P, lane); break;
+          case 3: key_string<3, ADD>(dst + off, src + off, mv.raw, P, lane); break;
+          default: key_string<4, ADD>(dst + off, src + off, mv.raw, P, lane); break;
+        }
       }
     } else {
-      const int off = L.vcode_off;
+      uint8_t* d = dst + L.vcode_off;
       switch (L.v_rate) {
-        case 1: value_string<1>(dst + off, src + off, info, it - nq, lane); break;
-        case 2: value_string<2>(dst + off, src + off, info, it - nq, lane); break;
-        case 3: value_string<3>(dst + off, src + off, info, it - nq, lane); break;
-        default: value_string<4>(dst + off, src + off, info, it - nq, lane); break;
+        case 1: value_string<1, ADD>(d, src, mv.value, it - nq, lane); break;
+        case 2: value_string<2, ADD>(d, src, mv.value, it - nq, lane); break;
+        case 3: value_string<3, ADD>(d, src, mv.value, it - nq, lane); break;
+        default: value_string<4, ADD>(d, src, mv.value, it - nq, lane); break;
       }
     }
   }
   // norm rows of the key groups, then of the values: token g + 8 m of a row at entry 8 g + m
-  for (int e = tid; e < (L.n_kgroups + 1) * kTile; e += kMoveThreads) {
-    const int row = e >> 6, en = e & 63, x = info[(en >> 3) + 8 * (en & 7)];
-    if (x < 0) continue;
-    const int tok = x & 63, es = row * kTile + (tok & 7) * 8 + (tok >> 3);
-    const uint8_t* s = src + (x - tok) + L.knorm_off;
-    if (L.norm_fp16)
-      reinterpret_cast<unsigned short*>(dst + L.knorm_off)[e] = reinterpret_cast<const unsigned short*>(s)[es];
-    else
-      reinterpret_cast<unsigned*>(dst + L.knorm_off)[e] = reinterpret_cast<const unsigned*>(s)[es];
+  // (a token without a source adds the zeros it points at)
+  const int t = tid & 63, en = (t & 7) * 8 + (t >> 3);
+  const uint8_t* s = src + mv.norm[t];
+#pragma unroll 1
+  for (int row = tid >> 6; row <= L.n_kgroups; row += NT / 64) {
+    if (L.norm_fp16) put<ADD>(reinterpret_cast<unsigned short*>(dst + L.knorm_off) + row * kTile + en, reinterpret_cast<const unsigned short*>(s)[row * kTile]);
+    else put<ADD>(reinterpret_cast<unsigned*>(dst + L.knorm_off) + row * kTile + en, reinterpret_cast<const unsigned*>(s)[row * kTile]);
   }
 }
 
+template <int NT>
 __device__ __forceinline__ void zero_tile(uint8_t* p, int bytes) {
-  for (int i = threadIdx.x; i < bytes / 16; i += kMoveThreads) reinterpret_cast<uint4*>(p)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < bytes / 16; i += NT) reinterpret_cast<uint4*>(p)[i] = make_uint4(0, 0, 0, 0);
 }
+template <int NT>
 __device__ __forceinline__ void write_tile(uint8_t* out, const uint8_t* p, int bytes) {
-  for (int i = threadIdx.x; i < bytes / 16; i += kMoveThreads)
+  for (int i = threadIdx.x; i < bytes / 16; i += NT)
     reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(p)[i];
 }
 
@@ -206,14 +309,15 @@ __device__ __forceinline__ int row_tokens(const int* seq_lens, int b, long long 
 // into shared memory whole before anything is written, so a path may name its nodes in any
 // order. A path that leaves every token in its place writes nothing. Latency bound: one
 // round trip to memory for the lengths and the path, one for the tiles.
-__global__ void __launch_bounds__(kMoveThreads) commit_kernel(DevLayout L, CacheRef cache, const int* __restrict__ path,
+__global__ void __launch_bounds__(kCommitThreads) commit_kernel(DevLayout L, const __grid_constant__ QuadList ql, CacheRef cache, const int* __restrict__ path,
                                                               int path_ld, const int* __restrict__ n_path,
                                                               const int* __restrict__ n_nodes, int n_q,
                                                               const int* __restrict__ seq_lens,
                                                               int* __restrict__ new_lens, int h_kv) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(8) unsigned long long bar;
-  __shared__ int s_path[64], s_info[2][64], s_state;
+  __shared__ int s_path[64], s_state;
+  __shared__ __align__(8) Moves s_mv[2];
   const int tid = threadIdx.x, b = blockIdx.x / h_kv, h = blockIdx.x % h_kv, TB = L.tile_bytes;
   if (tid == 0) {
     mbar_init(&bar, 1);
@@ -253,10 +357,9 @@ __global__ void __launch_bounds__(kMoveThreads) commit_kernel(DevLayout L, Cache
     // token `place` of the two tiles, counted from the first one's start
     const int place = tid, off = int(base - (long long)t0 * kTile);
     const int from = place >= off && place < off + a ? off + s_path[place - off] : place;
-    s_info[tid >> 6][tid & 63] = (from >> 6) * TB + (from & 63);
+    set_move(L, s_mv[tid >> 6], tid & 63, (from >> 6) * TB, from & 63);
   }
-  zero_tile(made, 2 * TB);
-  const bool ok = mbar_wait_bounded(&bar, 0);
+  const bool ok = tid < 32 ? mbar_wait_bounded(&bar, 0) : true;  // (one warp polls)
   if (__syncthreads_or(!ok)) {
     if (tid == 0) {
       atomicOr(L.status, BGTQ_STATUS_TIMEOUT);
@@ -265,11 +368,11 @@ __global__ void __launch_bounds__(kMoveThreads) commit_kernel(DevLayout L, Cache
     __syncthreads();
     return;
   }
-  assemble_tile(L, made, in, s_info[0]);
-  if (last > t0) assemble_tile(L, made + TB, in, s_info[1]);
+  assemble_tile<kCommitThreads, false>(L, ql, made, in, s_mv[0]);
+  if (last > t0) assemble_tile<kCommitThreads, false>(L, ql, made + TB, in, s_mv[1]);
   __syncthreads();
-  write_tile(tile[0], made, TB);
-  if (last > t0) write_tile(tile[1], made + TB, TB);
+  write_tile<kCommitThreads>(tile[0], made, TB);
+  if (last > t0) write_tile<kCommitThreads>(tile[1], made + TB, TB);
 }
 
 // ------------------------------------------------------------------ eviction: selection
@@ -304,7 +407,7 @@ struct SelectArgs {
   unsigned* status;
 };
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectArgs a) {
   extern __shared__ __align__(16) unsigned s_keys[];   // a.cached keys
   __shared__ __align__(16) int s_hist[kBins];
   __shared__ int s_warp[2][kSelWarps], s_find[2], s_total[2];
@@ -335,7 +438,17 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
     return i < a.n_sink || i >= n - a.n_recent ? 0xffffffffu : mass_key(mass[i]);
   };
   auto key = [&](int i) { return i - c0 < a.cached ? s_keys[i - c0] : make_key(i); };
-  for (int i = c0 + tid; i < min(c1, c0 + a.cached); i += kSelThreads) s_keys[i - c0] = make_key(i);
+  {
+    const int ce = min(c1, c0 + a.cached);
+    for (int i0 = c0 + tid; i0 < ce; i0 += 8 * kSelThreads) {  // eight loads in flight
+      unsigned k[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) k[j] = i0 + j * kSelThreads < ce ? make_key(i0 + j * kSelThreads) : 0u;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i0 + j * kSelThreads < ce) s_keys[i0 + j * kSelThreads - c0] = k[j];
+    }
+  }
 
   unsigned prefix = 0;
   int need = a.keep;   // tokens to take among those whose higher digits equal the prefix
@@ -457,68 +570,66 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
 // One CTA per destination tile. Bound by memory: the tiles that hold kept tokens are read
 // once (a tile that serves two destination tiles comes from L2 the second time), the kept
 // tokens are written once.
-__global__ void __launch_bounds__(kMoveThreads) gather_kernel(DevLayout L, CacheRef src, CacheRef dst,
+__global__ void __launch_bounds__(kGatherThreads) gather_kernel(DevLayout L, const __grid_constant__ QuadList ql, CacheRef src, CacheRef dst,
                                                               const int* __restrict__ kept,
                                                               const int* __restrict__ seq_lens, long long most,
                                                               int keep, int h_kv) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(8) unsigned long long bar;
-  __shared__ int s_tile[64], s_slot[64], s_tok[64], s_info[64], s_cnt[2];
+  __shared__ int s_tile[64], s_src[64], s_cnt[2];
+  __shared__ __align__(8) Moves s_mv;
   const int tid = threadIdx.x, lane = tid & 31, j = blockIdx.x, u = blockIdx.y, b = u / h_kv, h = u % h_kv;
   const int TB = L.tile_bytes;
   uint8_t* made = smem;
-  uint8_t* in = smem + TB;
+  uint8_t* in = smem + TB;                        // kMoveSlots source tiles, then one of zeros
   if (tid == 0) {
     mbar_init(&bar, 1);
     fence_mbar_init();
   }
-  zero_tile(made, TB);
   pdl_wait();  // the kept tokens come from the selection
   const int n = row_tokens(seq_lens, b, most), n_new = min(n, keep);
   if (j * kTile >= n_new) return;
   // the source tiles in order: slot of a token = distinct tiles before its own
-  int idx = -1;
+  int idx = -1, slot = -1;
   if (tid < 64) {
     if (j * kTile + tid < n_new) idx = kept[(size_t)u * keep + j * kTile + tid];
     if (idx >= n) idx = -1;
     s_tile[tid] = idx >> 6;  // (-1 stays -1)
-    s_tok[tid] = idx & 63;
   }
   __syncthreads();
   unsigned firsts = 0;
+  bool first = false;
   if (tid < 64) {
-    const bool first = idx >= 0 && (tid == 0 || s_tile[tid] != s_tile[tid - 1]);
+    first = idx >= 0 && (tid == 0 || s_tile[tid] != s_tile[tid - 1]);
     firsts = __ballot_sync(0xffffffffu, first);
     if (lane == 0) s_cnt[tid >> 5] = __popc(firsts);
   }
   __syncthreads();
-  if (tid < 64) {
-    const int s = (tid >= 32 ? s_cnt[0] : 0) + __popc(firsts & (0xffffffffu >> (31 - lane))) - 1;
-    s_slot[tid] = idx >= 0 ? s : -1;
+  const int n_slots = s_cnt[0] + s_cnt[1];
+  if (tid < 64 && idx >= 0) {
+    slot = (tid >= 32 ? s_cnt[0] : 0) + __popc(firsts & (0xffffffffu >> (31 - lane))) - 1;
+    if (first) s_src[slot] = idx >> 6;
   }
   __syncthreads();
-  const int n_slots = s_cnt[0] + s_cnt[1];
+  // a token without a source in a batch points at zeros
+  if (n_slots > kMoveSlots || j * kTile + kTile > n_new || src.table) zero_tile<kGatherThreads>(in + kMoveSlots * TB, TB);
   unsigned phase = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < n_slots; b0 += kMoveSlots, phase ^= 1u) {
     const int cnt = min(kMoveSlots, n_slots - b0);
     if (tid < 64) {
-      const int s = s_slot[tid] - b0;
-      s_info[tid] = s_slot[tid] >= 0 && s >= 0 && s < cnt && tile_present(src, b, s_tile[tid]) ? s * TB + s_tok[tid] : -1;
+      const bool here = slot >= b0 && slot < b0 + cnt && tile_present(src, b, idx >> 6);
+      set_move(L, s_mv, tid, here ? (slot - b0) * TB : kMoveSlots * TB, here ? idx & 63 : 0);
     }
-    if (tid < 32) {
-      // lane s: source tile of slot b0 + s (the first token with that slot names it)
-      const uint8_t* p = nullptr;
-      if (lane < cnt) {
-        int i = 0;
-        while (s_slot[i] != b0 + lane) ++i;
-        p = tile_ptr(src, L, b, h, h_kv, s_tile[i]);
-      }
+    bool ok = true;
+    if (tid < 32) {  // lane s brings the source tile of slot b0 + s; only this warp waits
+      const uint8_t* p = lane < cnt ? tile_ptr(src, L, b, h, h_kv, s_src[b0 + lane]) : nullptr;
       const int live = __popc(__ballot_sync(0xffffffffu, p != nullptr));
       if (lane == 0) mbar_expect_tx(&bar, unsigned(TB) * unsigned(live));
       __syncwarp();
       if (p) bulk_load(in + lane * TB, p, TB, &bar, evict_first_policy());
+      ok = mbar_wait_bounded(&bar, phase);
     }
-    const bool ok = mbar_wait_bounded(&bar, phase);
     if (__syncthreads_or(!ok)) {
       if (tid == 0) {
         atomicOr(L.status, BGTQ_STATUS_TIMEOUT);
@@ -527,11 +638,12 @@ __global__ void __launch_bounds__(kMoveThreads) gather_kernel(DevLayout L, Cache
       __syncthreads();
       return;
     }
-    assemble_tile(L, made, in, s_info);
+    if (b0 == 0) assemble_tile<kGatherThreads, false>(L, ql, made, in, s_mv);
+    else assemble_tile<kGatherThreads, true>(L, ql, made, in, s_mv);
     __syncthreads();
   }
   uint8_t* out = tile_ptr(dst, L, b, h, h_kv, j);
-  if (out) write_tile(out, made, TB);
+  if (out) write_tile<kGatherThreads>(out, made, TB);
 }
 
 int optin_smem(int* dev_out) {
@@ -566,8 +678,8 @@ cudaError_t launch_commit(const DevLayout& L, int batch, int h_kv, const int* pa
   static bool done[64] = {};
   cudaError_t e = raise_limit(commit_kernel, done);
   if (e != cudaSuccess) return e;
-  commit_kernel<<<unsigned(batch * h_kv), kMoveThreads, 4 * L.tile_bytes, stream>>>(
-      L, cache, path, path_ld, n_path, n_nodes, n_q, seq_lens, new_lens, h_kv);
+  commit_kernel<<<unsigned(batch * h_kv), kCommitThreads, 4 * L.tile_bytes, stream>>>(
+      L, quad_list(L), cache, path, path_ld, n_path, n_nodes, n_q, seq_lens, new_lens, h_kv);
   return cudaGetLastError();
 }
 
@@ -580,9 +692,9 @@ cudaError_t launch_evict(const DevLayout& L, int batch, int h_kv, const CacheRef
   if (e == cudaSuccess) e = raise_limit(gather_kernel, gat_done);
   if (e != cudaSuccess) return e;
   const int units = batch * h_kv;
-  // CTAs per unit: enough to fill the SMs or to leave each at most 4096 tokens, 8 at most
+  // CTAs per unit: enough to fill the SMs or to leave each at most 2048 tokens, 8 at most
   int cluster = 1;
-  while (cluster < 8 && units * cluster < num_sms && max_seq_len > 4096LL * cluster) cluster *= 2;
+  while (cluster < 8 && units * cluster < num_sms && max_seq_len > 2048LL * cluster) cluster *= 2;
   const long long per = (max_seq_len + cluster - 1) / cluster + 31;
   SelectArgs a{mass, mass_ld, max_seq_len, seq_lens, h_kv, keep, n_sink, n_recent, cluster,
                int(std::min<long long>(per, 24 * 1024)), kept, mass_out, mass_out_ld, new_lens, L.status};
@@ -604,15 +716,15 @@ cudaError_t launch_evict(const DevLayout& L, int batch, int h_kv, const CacheRef
   if (!tiles) return cudaSuccess;  // no row holds a token
   cudaLaunchConfig_t gcfg = {};
   gcfg.gridDim = dim3(unsigned(tiles), unsigned(units));
-  gcfg.blockDim = dim3(kMoveThreads);
-  gcfg.dynamicSmemBytes = size_t(kMoveSlots + 1) * L.tile_bytes;
+  gcfg.blockDim = dim3(kGatherThreads);
+  gcfg.dynamicSmemBytes = size_t(kMoveSlots + 2) * L.tile_bytes;
   gcfg.stream = stream;
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   gcfg.attrs = pdl;
   gcfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&gcfg, gather_kernel, L, src, dst, (const int*)kept, seq_lens, max_seq_len, keep, h_kv);
+  return cudaLaunchKernelEx(&gcfg, gather_kernel, L, quad_list(L), src, dst, (const int*)kept, seq_lens, max_seq_len, keep, h_kv);
 }
 
 }  // namespace bgtq
