@@ -834,7 +834,7 @@ bool tree_shape(int batch, int n_q, int h_q, int h_kv, long long max_seq_len) {
   if (batch <= 0 || h_kv <= 0 || h_q <= 0 || h_q % h_kv || h_q / h_kv > kMaxCols) return false;
   if (n_q < 1 || n_q > BGTQ_MAX_TREE || max_seq_len < 0) return false;
   const long long ct = ((long long)(h_q / h_kv) * n_q + kMaxG - 1) / kMaxG;
-  return (long long)batch * h_kv * ct <= 0x7fffffffLL / (kMaxG * 2);
+  return (long long)batch * h_kv * ct <= 0x7fffffffLL / 128;
 }
 
 // Query columns of a KV head (node x query head) from which a tree call takes the tcgen05

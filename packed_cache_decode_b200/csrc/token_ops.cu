@@ -450,6 +450,18 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectArgs a) {
     }
   }
 
+  // fn(key) for every key of the CTA, the cached ones four at a time
+  const int nc = min(c1 - c0, a.cached);
+  auto for_keys = [&](auto fn) {
+    for (int i = 4 * tid; i < nc; i += 4 * kSelThreads) {
+      const uint4 k = *reinterpret_cast<const uint4*>(s_keys + i);
+      fn(k.x);
+      if (i + 1 < nc) fn(k.y);
+      if (i + 2 < nc) fn(k.z);
+      if (i + 3 < nc) fn(k.w);
+    }
+    for (int i = c0 + nc + tid; i < c1; i += kSelThreads) fn(make_key(i));
+  };
   unsigned prefix = 0;
   int need = a.keep;   // tokens to take among those whose higher digits equal the prefix
 #pragma unroll
@@ -458,10 +470,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectArgs a) {
     const unsigned above = pass == 0 ? 0u : 0xffffffffu << (shift + bits);
     reinterpret_cast<int4*>(s_hist)[tid] = make_int4(0, 0, 0, 0);
     __syncthreads();
-    for (int i = c0 + tid; i < c1; i += kSelThreads) {
-      const unsigned k = key(i);
+    for_keys([&](unsigned k) {
       if ((k & above) == prefix) atomicAdd(&s_hist[(k >> shift) & ((1u << bits) - 1u)], 1);
-    }
+    });
     cl.sync();
     // thread t: bins 4 (511 - t) .. + 3, the highest digits first
     const int at = kSelThreads - 1 - tid;
@@ -494,11 +505,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectArgs a) {
   }
   // prefix: the threshold; need: how many of the tokens equal to it are kept
   int gt = 0, eq = 0;
-  for (int i = c0 + tid; i < c1; i += kSelThreads) {
-    const unsigned k = key(i);
+  for_keys([&](unsigned k) {
     gt += k > prefix;
     eq += k == prefix;
-  }
+  });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     gt += __shfl_xor_sync(0xffffffffu, gt, o);
@@ -697,7 +707,7 @@ cudaError_t launch_evict(const DevLayout& L, int batch, int h_kv, const CacheRef
   while (cluster < 8 && units * cluster < num_sms && max_seq_len > 2048LL * cluster) cluster *= 2;
   const long long per = (max_seq_len + cluster - 1) / cluster + 31;
   SelectArgs a{mass, mass_ld, max_seq_len, seq_lens, h_kv, keep, n_sink, n_recent, cluster,
-               int(std::min<long long>(per, 24 * 1024)), kept, mass_out, mass_out_ld, new_lens, L.status};
+               int(std::min<long long>((per + 3) / 4 * 4, 24 * 1024)), kept, mass_out, mass_out_ld, new_lens, L.status};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(units * cluster));
   cfg.blockDim = dim3(kSelThreads);

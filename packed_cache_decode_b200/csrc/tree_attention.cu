@@ -80,6 +80,8 @@ struct TreeLaunch {
   long long most;              // tokens a row may have in this call
   int batch, h_kv, G, n_q;     // G: query heads per KV head
   int col_tiles, row_units;    // 128-column tiles per KV head; units per row
+  unsigned quad[kMaxQuads];    // key quads: byte offset | pairs << 16 | group << 20 | rate << 24
+  unsigned char range[kDecGroup][5][2];  // key quads of each decode warp, by rate
   int q_words;                 // words per part (hi or lo) of a column: 4 per quad, quads even
   int stages;
 };
@@ -394,41 +396,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
       st_s32(k_at + unsigned(i >> 8) * k_part + unsigned(nq) * 1024u + 4u * (i & 255), 0u);
 #pragma unroll 1
   for (int it = warp; it < nq; it += kTreeThreads / 32) {
-    int gi = 0;
-#pragma unroll 1
-    while (gi + 1 < L.n_kgroups && it >= L.group_quad0[gi + 1]) ++gi;
-    const int r = L.group_rate[gi], P = L.quad_np[it], g = lane >> 2, t4 = lane & 3;
+    const unsigned qi = a.quad[it], qo = qi & 0xffffu;
+    const int r = qi >> 24, P = qi >> 16 & 15u, gi = qi >> 20 & 15u, g = lane >> 2, t4 = lane & 3;
     const unsigned li = t4 < P ? g * P + t4 : 0u;  // (a lane without a pair: any code, its q' is zero)
-    const unsigned qo = unsigned(L.quad_off[it]);
     const unsigned off = r == 3 ? (qo + 4u * li) | ((qo + 32u * P + 2u * li) << 16) : qo + 2u * r * li;
     st_s32(u_at + 8u * (it * 32 + lane), off);
     st_s32(u_at + 8u * (it * 32 + lane) + 4u, unsigned(gi * kTile * 8 + 16 * g));
   }
-  if (tid < kDecGroup) {
-    // the quads lie in descending rate; each decode warp takes a run of about equal cost
-    // (instructions per quad of rate 1..4), so that it and its partner in the other group,
-    // on the same scheduler, stay with the code of one or two rates
-    auto cost = [](int r) { return r == 1 ? 6 : r == 2 ? 7 : 11; };
-    auto rate_of = [&](int it) {
-      int gi = 0;
-#pragma unroll 1
-      while (gi + 1 < L.n_kgroups && it >= L.group_quad0[gi + 1]) ++gi;
-      return L.group_rate[gi];
-    };
-    int total = 0, run = 0;
-#pragma unroll 1
-    for (int it = 0; it < nq; ++it) total += cost(rate_of(it));
-#pragma unroll 1
-    for (int r = 0; r < 5; ++r) s.range[tid][r][0] = s.range[tid][r][1] = 0;
-#pragma unroll 1
-    for (int it = 0; it < nq; ++it) {
-      const int r = rate_of(it), c = cost(r), owner = min(kDecGroup - 1, (2 * run + c) * kDecGroup / (2 * total));
-      run += c;
-      if (owner != tid) continue;
-      if (s.range[tid][r][1] == 0) s.range[tid][r][0] = it;
-      s.range[tid][r][1] = it + 1;
-    }
-  }
+  if (tid < kDecGroup * 10) s.range[tid / 10][tid % 10 / 2][tid % 2] = a.range[tid / 10][tid % 10 / 2][tid % 2];
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   tc_fence_before();
   __syncthreads();
@@ -889,24 +864,27 @@ ValueLane<VR> vl;
   __syncthreads();
 }
 
-// Rows' tile prefix (block 0) and Q' of 32 query columns per block (row, KV head). The key
+// Rows' tile prefix (block 0) and Q' of COLS query columns per block (row, KV head). The key
 // rotations come into shared memory whole, their loads in flight together with the queries;
-// thread (packed dim p, half) then sums R_g[i][j] q[j] for 16 columns, a power of two per
+// thread (packed dim p, half) then sums R_g[i][j] q[j] for half of them, a power of two per
 // column brings its largest entry near 2^13, and the fp16 hi and lo words go out in
 // tensor-memory order. Latency bound: 512 blocks of the 70B-shaped layer with 64 nodes.
-constexpr int kPrepCols = 32;
-constexpr int kColLd = kPrepCols + 4;   // row of 32 columns in shared memory, 16-byte aligned
-constexpr int kPrepSmem = (kD * kD + kD * kColLd) * int(sizeof(float));
+// COLS columns per block: 32, or 8 where 32 would leave SMs without one.
+template <int COLS>
+constexpr int kColLd = COLS + 4;   // row of columns in shared memory, 16-byte aligned
+template <int COLS>
+constexpr int kRotSmem = (kD * kD + kD * kColLd<COLS>) * int(sizeof(float));
+template <int COLS>
 __global__ void __launch_bounds__(256) tree_prep_kernel(DevLayout L, TreeLaunch a, const void* __restrict__ q, int q_dtype,
                                                         float qscale, long long* __restrict__ prefix,
                                                         unsigned* __restrict__ qt, float* __restrict__ q_scale) {
   extern __shared__ __align__(128) unsigned char smem[];
   float* s_rot = reinterpret_cast<float*>(smem);      // the groups' rotations, transposed, one after the other
   float* s_q = s_rot + kD * kD;                       // [packed dim][column], then q' likewise
-  __shared__ float s_up[kPrepCols];
+  __shared__ float s_up[COLS];
   __shared__ short s_pc[kD], s_dim[kMaxDims];
   pdl_trigger();
-  const int tid = threadIdx.x, N = a.G * a.n_q, blocks = a.col_tiles * (kCols / kPrepCols);
+  const int tid = threadIdx.x, N = a.G * a.n_q, blocks = a.col_tiles * (kCols / COLS);
   if (blockIdx.x == 0 && tid < 32) {
     long long run = 0;
 #pragma unroll 1
@@ -931,14 +909,14 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(DevLayout L, TreeLaunch 
     if (tid == 0) prefix[0] = 0;
   }
   const int cb = blockIdx.x % blocks, bh = blockIdx.x / blocks, h = bh % a.h_kv, b = bh / a.h_kv;
-  const int c0 = cb * kPrepCols;
+  const int c0 = cb * COLS;
   const long long u = (long long)b * a.row_units + (long long)h * a.col_tiles + c0 / kCols;
   const int in0 = c0 % kCols;  // first column inside the unit
   const int qw = a.q_words;
   if (c0 >= N) {  // columns that no query has: zeros
-    for (int e = tid; e < kPrepCols * 2 * qw / 4; e += 256)
-      reinterpret_cast<uint4*>(qt)[((size_t)u * (2 * qw / 4) + e / kPrepCols) * kCols + in0 + e % kPrepCols] = make_uint4(0, 0, 0, 0);
-    if (tid < kPrepCols) q_scale[(size_t)u * kCols + in0 + tid] = 1.f;
+    for (int e = tid; e < COLS * 2 * qw / 4; e += 256)
+      reinterpret_cast<uint4*>(qt)[((size_t)u * (2 * qw / 4) + e / COLS) * kCols + in0 + e % COLS] = make_uint4(0, 0, 0, 0);
+    if (tid < COLS) q_scale[(size_t)u * kCols + in0 + tid] = 1.f;
     return;
   }
   for (int g = 0, at = 0; g < L.n_kgroups; ++g) {
@@ -953,20 +931,20 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(DevLayout L, TreeLaunch 
   for (int e = tid; e < 8 * L.n_kquads; e += 256) s_dim[e] = (e & 7) < 2 * L.quad_np[e >> 3] ? short(L.quad_dim0[e >> 3] + (e & 7)) : short(-1);
   __syncthreads();
 #pragma unroll 8
-  for (int e = tid; e < kPrepCols * kD; e += 256) {
+  for (int e = tid; e < COLS * kD; e += 256) {
     const int c = e >> 7, p = e & (kD - 1), col = c0 + c;
     float x = 0.f;
     if (col < N && p < L.n_packed) {
       const size_t r = ((size_t)b * a.n_q + col / a.G) * (a.G * a.h_kv) + (size_t)h * a.G + col % a.G;
       x = load_q(q, q_dtype, r * kD + s_pc[p]);
     }
-    s_q[p * kColLd + c] = x;
+    s_q[p * kColLd<COLS> + c] = x;
   }
   __syncthreads();
   const int p = tid & (kD - 1), half = tid >> 7;
-  float acc[16];
+  float acc[COLS / 2];
 #pragma unroll
-  for (int c = 0; c < 16; ++c) acc[c] = 0.f;
+  for (int c = 0; c < COLS / 2; ++c) acc[c] = 0.f;
   float f = 0.f;
   if (p < L.n_packed) {
     int g = 0, at = 0;
@@ -976,14 +954,14 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(DevLayout L, TreeLaunch 
     }
     const int d = L.group_dim[g], off = L.group_off[g];
     const float* R = s_rot + at + (p - off);
-    const float* x = s_q + off * kColLd + 16 * half;
+    const float* x = s_q + off * kColLd<COLS> + COLS / 2 * half;
     f = qscale * rsqrtf(float(d)) * L.inv_kappa_group[g];
 #pragma unroll 4
     for (int j = 0; j < d; ++j) {
       const float r = R[j * d];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 v = *reinterpret_cast<const float4*>(x + j * kColLd + 4 * k);
+      for (int k = 0; k < COLS / 8; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(x + j * kColLd<COLS> + 4 * k);
         acc[4 * k] = fmaf(r, v.x, acc[4 * k]);
         acc[4 * k + 1] = fmaf(r, v.y, acc[4 * k + 1]);
         acc[4 * k + 2] = fmaf(r, v.z, acc[4 * k + 2]);
@@ -993,15 +971,15 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(DevLayout L, TreeLaunch 
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    *reinterpret_cast<float4*>(s_q + p * kColLd + 16 * half + 4 * k) =
+  for (int k = 0; k < COLS / 8; ++k)
+    *reinterpret_cast<float4*>(s_q + p * kColLd<COLS> + COLS / 2 * half + 4 * k) =
         make_float4(acc[4 * k] * f, acc[4 * k + 1] * f, acc[4 * k + 2] * f, acc[4 * k + 3] * f);
   __syncthreads();
-  if (tid < 8 * kPrepCols) {  // eight threads per column
+  if (tid < 8 * COLS) {  // eight threads per column
     const int c = tid >> 3;
     float top = 0.f;
     for (int e = tid & 7; e < kD; e += 8) {
-      const float x = fabsf(s_q[e * kColLd + c]);
+      const float x = fabsf(s_q[e * kColLd<COLS> + c]);
       if (x <= 3.0e38f) top = fmaxf(top, x);  // (an infinite or NaN q' keeps its column so)
     }
 #pragma unroll
@@ -1014,8 +992,8 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(DevLayout L, TreeLaunch 
   }
   __syncthreads();
   // word w of a column's part = operand dims 2w, 2w + 1; groups of 4 words, columns innermost
-  for (int e = tid; e < kPrepCols * qw / 4; e += 256) {
-    const int c = e % kPrepCols, w = e / kPrepCols;
+  for (int e = tid; e < COLS * qw / 4; e += 256) {
+    const int c = e % COLS, w = e / COLS;
     unsigned hi[4], lo[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -1023,7 +1001,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(DevLayout L, TreeLaunch 
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int od = 8 * w + 2 * k + i, dim = od < 8 * L.n_kquads ? s_dim[od] : -1;
-        v[i] = dim >= 0 ? s_q[dim * kColLd + c] * s_up[c] : 0.f;
+        v[i] = dim >= 0 ? s_q[dim * kColLd<COLS> + c] * s_up[c] : 0.f;
       }
       const float h0 = __half2float(__float2half_rn(v[0])), h1 = __half2float(__float2half_rn(v[1]));
       hi[k] = pack_h2(h0, h1);
@@ -1035,27 +1013,28 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(DevLayout L, TreeLaunch 
   }
 }
 
-// Merge of a unit's partials for 32 query columns per block, then out = R_V^T o' / l with the
+// Merge of a unit's partials for COLS query columns per block, then out = R_V^T o' / l with the
 // rotation in shared memory (fetched before the wait for the partials): thread (output dim,
-// half) sums 16 columns. Bound by its shared-memory reads and by latency.
-constexpr int kCombSmem = (kD * kD + kD * kColLd) * int(sizeof(float));
+// half) sums half of the columns. Bound by its shared-memory reads and by latency.
+template <int COLS>
 __global__ void __launch_bounds__(256) tree_combine_kernel(DevLayout L, TreeLaunch a, int n_ctas, void* __restrict__ out,
                                                            int out_dtype) {
   extern __shared__ __align__(128) unsigned char smem[];
   float* s_rot = reinterpret_cast<float*>(smem);   // R_V [i][d]
   float* s_o = s_rot + kD * kD;                    // [value dim][column]
-  const int tid = threadIdx.x, N = a.G * a.n_q, blocks = (N + kPrepCols - 1) / kPrepCols;
+  const int tid = threadIdx.x, N = a.G * a.n_q, blocks = (N + COLS - 1) / COLS;
   pdl_trigger();
 #pragma unroll
   for (int e = 0; e < kD * kD / 4 / 256; ++e)
     reinterpret_cast<float4*>(s_rot)[e * 256 + tid] = __ldg(reinterpret_cast<const float4*>(L.v_rot32) + e * 256 + tid);
   pdl_wait();
   const int cb = blockIdx.x % blocks, bh = blockIdx.x / blocks, h = bh % a.h_kv, b = bh / a.h_kv;
-  const int c0 = cb * kPrepCols, in0 = c0 % kCols;
+  const int c0 = cb * COLS, in0 = c0 % kCols;
   const long long k = (long long)h * a.col_tiles + c0 / kCols, u = (long long)b * a.row_units + k;
   const int n_nodes = a.tree.n_nodes ? a.tree.n_nodes[b] : a.n_q;
   const long long T = a.prefix[a.batch], C = min((long long)n_ctas, T), p0 = a.prefix[b], nt = (a.prefix[b + 1] - p0) / a.row_units;
-  const int c = tid & 31, wp = tid >> 5;  // merge: column c, float4s wp, wp + 8, ..
+  constexpr int kGroups = 256 / COLS, kVecs = 32 / kGroups;  // merge: column c, float4s wp, wp + kGroups, ..
+  const int c = tid % COLS, wp = tid / COLS;
   // (a row without tiles has no partials: zeros)
   int first = 0, n = 0;
   if (nt > 0) {
@@ -1066,22 +1045,22 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(DevLayout L, TreeLaun
   const float2* ml = a.part_ml + (size_t)(first + u) * kCols + in0 + c;
   const float4* po = a.part_o + ((size_t)(first + u) * 32 + wp) * kCols + in0 + c;
   float top = -INFINITY, l = 0.f;
-  float4 o[4];
+  float4 o[kVecs];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j = 0; j < kVecs; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
   // kSlots partials at a time, their loads in flight together; the running maximum as usual
-  constexpr int kSlots = 4;
+  constexpr int kSlots = COLS == 32 ? 4 : 16;
 #pragma unroll 1
   for (int s0 = 0; live && s0 < n; s0 += kSlots) {
     float2 v[kSlots];
-    float4 x[kSlots][4];
+    float4 x[kSlots][kVecs];
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
       const int sl = min(s0 + i, n - 1);
       v[i] = ml[(size_t)sl * kCols];
       if (s0 + i >= n) v[i] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[i][j] = __ldcs(po + ((size_t)sl * 32 + 8 * j) * kCols);
+      for (int j = 0; j < kVecs; ++j) x[i][j] = __ldcs(po + ((size_t)sl * 32 + kGroups * j) * kCols);
     }
     float m = top;
 #pragma unroll
@@ -1090,7 +1069,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(DevLayout L, TreeLaun
     const float r = exp2f(top - m);
     l *= r;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = make_float4(o[j].x * r, o[j].y * r, o[j].z * r, o[j].w * r);
+    for (int j = 0; j < kVecs; ++j) o[j] = make_float4(o[j].x * r, o[j].y * r, o[j].z * r, o[j].w * r);
     top = m;
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
@@ -1098,41 +1077,41 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(DevLayout L, TreeLaun
       const float f = exp2f(v[i].x - m);
       l = fmaf(f, v[i].y, l);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < kVecs; ++j)
         o[j] = make_float4(fmaf(f, x[i][j].x, o[j].x), fmaf(f, x[i][j].y, o[j].y), fmaf(f, x[i][j].z, o[j].z),
                            fmaf(f, x[i][j].w, o[j].w));
     }
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < kVecs; ++j) {
     // accumulator column n = 8 blk + g holds value dim 16 g + blk
     const float x[4] = {o[j].x, o[j].y, o[j].z, o[j].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int nn = 4 * (wp + 8 * j) + e;
-      s_o[(16 * (nn & 7) + (nn >> 3)) * kColLd + c] = x[e] * inv;
+      const int nn = 4 * (wp + kGroups * j) + e;
+      s_o[(16 * (nn & 7) + (nn >> 3)) * kColLd<COLS> + c] = x[e] * inv;
     }
   }
   __syncthreads();
   const int d = tid & (kD - 1), half = tid >> 7;
-  unsigned long long acc[8];
+  unsigned long long acc[COLS / 4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0ull;
+  for (int i = 0; i < COLS / 4; ++i) acc[i] = 0ull;
 #pragma unroll 8
   for (int i = 0; i < kD; ++i) {
     const float r = s_rot[i * kD + d];
     const unsigned long long rr = pack2(r, r);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float4 x = *reinterpret_cast<const float4*>(s_o + i * kColLd + 16 * half + 4 * e);
+    for (int e = 0; e < COLS / 8; ++e) {
+      const float4 x = *reinterpret_cast<const float4*>(s_o + i * kColLd<COLS> + COLS / 2 * half + 4 * e);
       acc[2 * e] = fma2(rr, pack2(x.x, x.y), acc[2 * e]);
       acc[2 * e + 1] = fma2(rr, pack2(x.z, x.w), acc[2 * e + 1]);
     }
   }
 #pragma unroll
-  for (int cc = 0; cc < 16; ++cc) {
-    const int col = c0 + 16 * half + cc, node = col / a.G;
+  for (int cc = 0; cc < COLS / 2; ++cc) {
+    const int col = c0 + COLS / 2 * half + cc, node = col / a.G;
     // rows past a row's drafted nodes are not written (a row that does not fit: zeros)
     if (col >= N || (n_nodes >= 0 && node >= n_nodes)) continue;
     const float2 y = unpack2(acc[cc >> 1]);
@@ -1142,6 +1121,23 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(DevLayout L, TreeLaun
 }
 
 int tree_q_words(const DevLayout& L) { return (L.n_kquads + 1) / 2 * 8; }
+
+// The layout's quads for the decode warps. They lie in descending rate; each warp of a group
+// takes a run of about equal cost (instructions per quad of rate 1..4), so that it and its
+// partner in the other group, on the same scheduler, stay with the code of one or two rates.
+void set_quads(const DevLayout& L, TreeLaunch& a) {
+  auto cost = [](int r) { return r == 1 ? 6 : r == 2 ? 7 : 11; };
+  int total = 0, run = 0, it = 0;
+  for (int g = 0; g < L.n_kgroups; ++g) total += L.group_nquads[g] * cost(L.group_rate[g]);
+  for (int g = 0; g < L.n_kgroups; ++g)
+    for (int i = 0; i < L.group_nquads[g]; ++i, ++it) {
+      const int r = L.group_rate[g], c = cost(r), w = std::min(kDecGroup - 1, (2 * run + c) * kDecGroup / (2 * total));
+      a.quad[it] = unsigned(L.quad_off[it]) | unsigned(L.quad_np[it]) << 16 | unsigned(g) << 20 | unsigned(r) << 24;
+      if (a.range[w][r][1] == 0) a.range[w][r][0] = (unsigned char)it;
+      a.range[w][r][1] = (unsigned char)(it + 1);
+      run += c;
+    }
+}
 
 int tree_smem_bytes(const DevLayout& L, int stages) {
   const int vt = L.v_rate == 3 ? vtab_bytes<3>() : L.v_rate == 4 ? vtab_bytes<4>() : 0;
@@ -1231,21 +1227,26 @@ cudaError_t launch_tree(const DevLayout& L, const TreePlan& plan, const void* q,
   a.col_tiles = plan.col_tiles;
   a.row_units = h_kv * plan.col_tiles;
   a.q_words = tree_q_words(L);
+  set_quads(L, a);
   const int limit = split_smem_limit();
   a.stages = kMaxStages;
   while (a.stages > 2 && tree_smem_bytes(L, a.stages) > limit) --a.stages;
   const int smem = tree_smem_bytes(L, a.stages);
   if (smem > limit) return cudaErrorInvalidValue;
-  const unsigned blocks = unsigned((long long)batch * h_kv * plan.col_tiles * (kCols / kPrepCols));
-  static bool prep_done[64] = {}, comb_done[64] = {};
-  cudaError_t e = raise_smem_limit(tree_prep_kernel, prep_done);
-  if (e == cudaSuccess) e = raise_smem_limit(tree_combine_kernel, comb_done);
-  if (e != cudaSuccess) return e;
-  tree_prep_kernel<<<blocks, 256, kPrepSmem, stream>>>(L, a, q, q_dtype, softmax_scale * kLog2e,
-                                               reinterpret_cast<long long*>(ws + plan.prefix_at),
-                                               reinterpret_cast<unsigned*>(ws + plan.q_at),
-                                               reinterpret_cast<float*>(ws + plan.scale_at));
-  e = cudaGetLastError();
+  const long long heads = (long long)batch * h_kv;
+  const int N = a.G * n_q;
+  const bool wide = heads * ((N + 31) / 32) >= plan.n_ctas;
+  auto prep = [&](auto cols) {
+    constexpr int COLS = decltype(cols)::value;
+    static bool done[64] = {};
+    const cudaError_t e = raise_smem_limit(tree_prep_kernel<COLS>, done);
+    if (e != cudaSuccess) return e;
+    tree_prep_kernel<COLS><<<unsigned(heads * plan.col_tiles * (kCols / COLS)), 256, kRotSmem<COLS>, stream>>>(
+        L, a, q, q_dtype, softmax_scale * kLog2e, reinterpret_cast<long long*>(ws + plan.prefix_at),
+        reinterpret_cast<unsigned*>(ws + plan.q_at), reinterpret_cast<float*>(ws + plan.scale_at));
+    return cudaGetLastError();
+  };
+  cudaError_t e = wide ? prep(IntC<32>{}) : prep(IntC<8>{});
   if (e != cudaSuccess) return e;
   const unsigned grid = unsigned(plan.n_ctas);
   auto go = [&](auto vr) {
@@ -1260,17 +1261,24 @@ cudaError_t launch_tree(const DevLayout& L, const TreePlan& plan, const void* q,
     default: e = go(IntC<4>{}); break;
   }
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((long long)batch * h_kv * ((a.G * n_q + kPrepCols - 1) / kPrepCols)));
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = kCombSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_combine_kernel, L, a, plan.n_ctas, out, out_dtype);
+  auto combine = [&](auto cols) {
+    constexpr int COLS = decltype(cols)::value;
+    static bool done[64] = {};
+    const cudaError_t e = raise_smem_limit(tree_combine_kernel<COLS>, done);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(heads * ((N + COLS - 1) / COLS)));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = kRotSmem<COLS>;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_combine_kernel<COLS>, L, a, plan.n_ctas, out, out_dtype);
+  };
+  return wide ? combine(IntC<32>{}) : combine(IntC<8>{});
 }
 
 }  // namespace bgtq

@@ -192,8 +192,21 @@ def reference_keep(mass, n, keep, n_sink, n_recent):
 
 
 def reference_tiles(olay, tiles, idx, n_tiles):
+    """Tiles of the tokens idx: codes through the oracle, norms as the bits they are (a norm may
+    be any bit pattern, NaN among them)."""
+    code, rows = 64 * (olay.k_record_bytes + olay.v_record_bytes), olay.n_kgroups + 1
     u = O.unpack(olay, tiles.reshape(-1), tiles.shape[0] * 64)
-    return O.pack(olay, {k: x[idx] for k, x in u.items()}, n_tiles * 64).reshape(n_tiles, -1)
+    kept = {k: np.zeros_like(x[idx]) if "norm" in k else x[idx] for k, x in u.items()}
+    out = O.pack(olay, kept, n_tiles * 64).reshape(n_tiles, -1)
+    it = np.uint16 if olay.norm_fp16 else np.uint32
+
+    def by_token(t):                     # [tiles, row, 8 g + m] -> [token g + 8 m, row]
+        return t[:, code:].copy().view(it).reshape(-1, rows, 8, 8).transpose(0, 3, 2, 1).reshape(-1, rows)
+
+    norms = np.zeros((n_tiles * 64, rows), it)
+    norms[:len(idx)] = by_token(tiles.reshape(-1, olay.tile_bytes))[idx]
+    out[:, code:] = norms.reshape(n_tiles, 8, 8, rows).transpose(0, 3, 2, 1).reshape(n_tiles, -1).copy().view(np.uint8).reshape(n_tiles, -1)
+    return out
 
 
 EVICT_CASES = [  # mix, v_rate, fp16, h_kv, lens, keep, sink, recent, kind of mass, paged
