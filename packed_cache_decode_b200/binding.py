@@ -329,6 +329,26 @@ def dtype_code(t) -> int:
     return _DTYPES[t.dtype]
 
 
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+def _raw_stream(stream):
+    """Address of the stream, or of the current device's current one, without a Stream object
+    (which costs more than the smallest of the calls takes on the GPU)."""
+    if stream is not None:
+        return stream.cuda_stream
+    torch = _torch()
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
 def _stream_ptr(stream):
     import torch
     s = stream if stream is not None else torch.cuda.current_stream()
@@ -715,11 +735,11 @@ def tree_workspace_bytes(layout: Layout, batch: int, h_q: int, h_kv: int, n_q: i
 
 
 def _opt(t):
-    return C.c_void_p(None if t is None else t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _tree_shapes(q, tree_mask, n_nodes, seq_lens, out):
-    import torch
+    torch = _torch()
     B_, n_q, h_q, d = q.shape
     assert d == HEAD_DIM and q.is_contiguous() and out.is_contiguous() and out.shape == q.shape
     assert tree_mask.dtype in (torch.int64, torch.uint64) and tuple(tree_mask.shape) == (B_, n_q)
@@ -736,11 +756,11 @@ def tree_attention(layout: Layout, q, tree_mask, cache, seq_lens, capacity: int,
     row); out like q (fp32, bf16 or fp16). Rows past a row's nodes are not written."""
     B_, n_q, h_q = _tree_shapes(q, tree_mask, n_nodes, seq_lens, out)
     scale = 1.0 / HEAD_DIM ** 0.5 if softmax_scale is None else float(softmax_scale)
-    _check(load().bgtq_tree_attention(layout.handle, C.c_void_p(q.data_ptr()), dtype_code(q), B_, n_q, h_q, h_kv,
-                                      C.c_void_p(tree_mask.data_ptr()), _opt(n_nodes), C.c_void_p(cache.data_ptr()),
-                                      C.c_void_p(seq_lens.data_ptr()), capacity, max_seq_len, scale,
-                                      C.c_void_p(out.data_ptr()), dtype_code(out), C.c_void_p(workspace.data_ptr()),
-                                      workspace.numel(), _stream_ptr(stream)), "tree_attention")
+    _check(load().bgtq_tree_attention(layout.handle, q.data_ptr(), dtype_code(q), B_, n_q, h_q, h_kv,
+                                      tree_mask.data_ptr(), _opt(n_nodes), cache.data_ptr(),
+                                      seq_lens.data_ptr(), capacity, max_seq_len, scale,
+                                      out.data_ptr(), dtype_code(out), workspace.data_ptr(),
+                                      workspace.numel(), _raw_stream(stream)), "tree_attention")
 
 
 def tree_attention_paged(layout: Layout, q, tree_mask, cache: PagedCache, seq_lens, max_seq_len: int, out, workspace,
@@ -748,18 +768,18 @@ def tree_attention_paged(layout: Layout, q, tree_mask, cache: PagedCache, seq_le
     B_, n_q, h_q = _tree_shapes(q, tree_mask, n_nodes, seq_lens, out)
     assert cache.table.shape[0] == B_
     scale = 1.0 / HEAD_DIM ** 0.5 if softmax_scale is None else float(softmax_scale)
-    _check(load().bgtq_tree_attention_paged(layout.handle, C.c_void_p(q.data_ptr()), dtype_code(q), B_, n_q, h_q, h_kv,
-                                            C.c_void_p(tree_mask.data_ptr()), _opt(n_nodes),
-                                            C.c_void_p(cache.pool.data_ptr()), cache.num_pages(layout, h_kv),
-                                            C.c_void_p(cache.table.data_ptr()), cache.max_pages,
-                                            C.c_void_p(seq_lens.data_ptr()), max_seq_len, scale,
-                                            C.c_void_p(out.data_ptr()), dtype_code(out),
-                                            C.c_void_p(workspace.data_ptr()), workspace.numel(), _stream_ptr(stream)),
+    _check(load().bgtq_tree_attention_paged(layout.handle, q.data_ptr(), dtype_code(q), B_, n_q, h_q, h_kv,
+                                            tree_mask.data_ptr(), _opt(n_nodes),
+                                            cache.pool.data_ptr(), cache.num_pages(layout, h_kv),
+                                            cache.table.data_ptr(), cache.max_pages,
+                                            seq_lens.data_ptr(), max_seq_len, scale,
+                                            out.data_ptr(), dtype_code(out),
+                                            workspace.data_ptr(), workspace.numel(), _raw_stream(stream)),
            "tree_attention_paged")
 
 
 def _commit_shapes(path, n_path, n_nodes, seq_lens, new_lens):
-    import torch
+    torch = _torch()
     B_, ld = path.shape
     for t in (path, n_path, seq_lens, new_lens) + (() if n_nodes is None else (n_nodes,)):
         assert t.dtype == torch.int32 and t.is_contiguous()
@@ -774,22 +794,22 @@ def tree_commit(layout: Layout, path, n_path, n_q: int, cache, seq_lens, new_len
     n_nodes[b], cached tokens) as the tokens after the prefix; new_lens [B] int32 CUDA
     receives the rows' lengths. path [B, >= n_q], n_path, seq_lens: int32 CUDA."""
     B_, ld = _commit_shapes(path, n_path, n_nodes, seq_lens, new_lens)
-    _check(load().bgtq_tree_commit(layout.handle, C.c_void_p(path.data_ptr()), ld, C.c_void_p(n_path.data_ptr()),
-                                   _opt(n_nodes), n_q, B_, h_kv, C.c_void_p(cache.data_ptr()),
-                                   C.c_void_p(seq_lens.data_ptr()), C.c_void_p(new_lens.data_ptr()), capacity,
-                                   _stream_ptr(stream)), "tree_commit")
+    _check(load().bgtq_tree_commit(layout.handle, path.data_ptr(), ld, n_path.data_ptr(),
+                                   _opt(n_nodes), n_q, B_, h_kv, cache.data_ptr(),
+                                   seq_lens.data_ptr(), new_lens.data_ptr(), capacity,
+                                   _raw_stream(stream)), "tree_commit")
 
 
 def tree_commit_paged(layout: Layout, path, n_path, n_q: int, cache: PagedCache, seq_lens, new_lens, h_kv: int,
                       n_nodes=None, stream=None):
     B_, ld = _commit_shapes(path, n_path, n_nodes, seq_lens, new_lens)
     assert cache.table.shape[0] == B_
-    _check(load().bgtq_tree_commit_paged(layout.handle, C.c_void_p(path.data_ptr()), ld,
-                                         C.c_void_p(n_path.data_ptr()), _opt(n_nodes), n_q, B_, h_kv,
-                                         C.c_void_p(cache.pool.data_ptr()), cache.num_pages(layout, h_kv),
-                                         C.c_void_p(cache.table.data_ptr()), cache.max_pages,
-                                         C.c_void_p(seq_lens.data_ptr()), C.c_void_p(new_lens.data_ptr()),
-                                         _stream_ptr(stream)), "tree_commit_paged")
+    _check(load().bgtq_tree_commit_paged(layout.handle, path.data_ptr(), ld,
+                                         n_path.data_ptr(), _opt(n_nodes), n_q, B_, h_kv,
+                                         cache.pool.data_ptr(), cache.num_pages(layout, h_kv),
+                                         cache.table.data_ptr(), cache.max_pages,
+                                         seq_lens.data_ptr(), new_lens.data_ptr(),
+                                         _raw_stream(stream)), "tree_commit_paged")
 
 
 # ---------------------------------------------------------------- a bounded cache
@@ -801,7 +821,7 @@ def mass_workspace_bytes(layout: Layout, batch: int, h_q: int, h_kv: int, max_se
 
 
 def _mass_shapes(q, mass, out, h_kv):
-    import torch
+    torch = _torch()
     B_, h_q, d = q.shape
     assert d == HEAD_DIM and q.is_contiguous() and out.is_contiguous() and out.shape == q.shape
     assert mass.dtype == torch.float32 and mass.is_contiguous() and tuple(mass.shape[:2]) == (B_, h_kv)
@@ -815,12 +835,12 @@ def decode_attention_mass(layout: Layout, q, cache, seq_lens, capacity: int, max
     q [B, h_q, 128]; out like q (fp32, bf16 or fp16)."""
     B_, h_q = _mass_shapes(q, mass, out, h_kv)
     scale = 1.0 / HEAD_DIM ** 0.5 if softmax_scale is None else float(softmax_scale)
-    _check(load().bgtq_decode_attention_mass(layout.handle, C.c_void_p(q.data_ptr()), dtype_code(q), B_, h_q, h_kv,
-                                             C.c_void_p(cache.data_ptr()), C.c_void_p(seq_lens.data_ptr()), capacity,
-                                             max_seq_len, scale, decay, C.c_void_p(mass.data_ptr()), mass.shape[2],
-                                             C.c_void_p(out.data_ptr()), dtype_code(out),
-                                             C.c_void_p(workspace.data_ptr()), workspace.numel(),
-                                             _stream_ptr(stream)), "decode_attention_mass")
+    _check(load().bgtq_decode_attention_mass(layout.handle, q.data_ptr(), dtype_code(q), B_, h_q, h_kv,
+                                             cache.data_ptr(), seq_lens.data_ptr(), capacity,
+                                             max_seq_len, scale, decay, mass.data_ptr(), mass.shape[2],
+                                             out.data_ptr(), dtype_code(out),
+                                             workspace.data_ptr(), workspace.numel(),
+                                             _raw_stream(stream)), "decode_attention_mass")
 
 
 def decode_attention_mass_paged(layout: Layout, q, cache: PagedCache, seq_lens, max_seq_len: int, mass, out,
@@ -829,18 +849,18 @@ def decode_attention_mass_paged(layout: Layout, q, cache: PagedCache, seq_lens, 
     B_, h_q = _mass_shapes(q, mass, out, h_kv)
     assert cache.table.shape[0] == B_
     scale = 1.0 / HEAD_DIM ** 0.5 if softmax_scale is None else float(softmax_scale)
-    _check(load().bgtq_decode_attention_mass_paged(layout.handle, C.c_void_p(q.data_ptr()), dtype_code(q), B_, h_q,
-                                                   h_kv, C.c_void_p(cache.pool.data_ptr()),
-                                                   cache.num_pages(layout, h_kv), C.c_void_p(cache.table.data_ptr()),
-                                                   cache.max_pages, C.c_void_p(seq_lens.data_ptr()), max_seq_len,
-                                                   scale, decay, C.c_void_p(mass.data_ptr()), mass.shape[2],
-                                                   C.c_void_p(out.data_ptr()), dtype_code(out),
-                                                   C.c_void_p(workspace.data_ptr()), workspace.numel(),
-                                                   _stream_ptr(stream)), "decode_attention_mass_paged")
+    _check(load().bgtq_decode_attention_mass_paged(layout.handle, q.data_ptr(), dtype_code(q), B_, h_q,
+                                                   h_kv, cache.pool.data_ptr(),
+                                                   cache.num_pages(layout, h_kv), cache.table.data_ptr(),
+                                                   cache.max_pages, seq_lens.data_ptr(), max_seq_len,
+                                                   scale, decay, mass.data_ptr(), mass.shape[2],
+                                                   out.data_ptr(), dtype_code(out),
+                                                   workspace.data_ptr(), workspace.numel(),
+                                                   _raw_stream(stream)), "decode_attention_mass_paged")
 
 
 def _evict_shapes(mass, mass_out, kept, seq_lens, new_lens, keep, h_kv):
-    import torch
+    torch = _torch()
     B_ = mass.shape[0]
     assert mass.dtype == torch.float32 and mass.is_contiguous() and mass.shape[1] == h_kv
     assert mass_out.dtype == torch.float32 and mass_out.is_contiguous() and tuple(mass_out.shape[:2]) == (B_, h_kv)
@@ -857,22 +877,22 @@ def cache_evict(layout: Layout, src, seq_lens, src_capacity: int, max_seq_len: i
     into dst, in their order. mass_out [B, h_kv, ld] fp32 receives their mass (then zeros),
     kept [B, h_kv, keep] int32 their old positions (then -1), new_lens [B] int32 the lengths."""
     B_ = _evict_shapes(mass, mass_out, kept, seq_lens, new_lens, keep, h_kv)
-    _check(load().bgtq_cache_evict(layout.handle, B_, h_kv, C.c_void_p(src.data_ptr()), src_capacity,
-                                   C.c_void_p(seq_lens.data_ptr()), max_seq_len, C.c_void_p(mass.data_ptr()),
-                                   mass.shape[2], keep, n_sink, n_recent, C.c_void_p(dst.data_ptr()), dst_capacity,
-                                   C.c_void_p(mass_out.data_ptr()), mass_out.shape[2], C.c_void_p(kept.data_ptr()),
-                                   C.c_void_p(new_lens.data_ptr()), _stream_ptr(stream)), "cache_evict")
+    _check(load().bgtq_cache_evict(layout.handle, B_, h_kv, src.data_ptr(), src_capacity,
+                                   seq_lens.data_ptr(), max_seq_len, mass.data_ptr(),
+                                   mass.shape[2], keep, n_sink, n_recent, dst.data_ptr(), dst_capacity,
+                                   mass_out.data_ptr(), mass_out.shape[2], kept.data_ptr(),
+                                   new_lens.data_ptr(), _raw_stream(stream)), "cache_evict")
 
 
 def cache_evict_paged(layout: Layout, src: PagedCache, seq_lens, max_seq_len: int, mass, keep: int, n_sink: int,
                       n_recent: int, dst: PagedCache, mass_out, kept, new_lens, h_kv: int, stream=None):
     B_ = _evict_shapes(mass, mass_out, kept, seq_lens, new_lens, keep, h_kv)
     assert src.table.shape[0] == B_ and dst.table.shape[0] == B_
-    _check(load().bgtq_cache_evict_paged(layout.handle, B_, h_kv, C.c_void_p(src.pool.data_ptr()),
-                                         src.num_pages(layout, h_kv), C.c_void_p(src.table.data_ptr()), src.max_pages,
-                                         C.c_void_p(seq_lens.data_ptr()), max_seq_len, C.c_void_p(mass.data_ptr()),
-                                         mass.shape[2], keep, n_sink, n_recent, C.c_void_p(dst.pool.data_ptr()),
-                                         dst.num_pages(layout, h_kv), C.c_void_p(dst.table.data_ptr()), dst.max_pages,
-                                         C.c_void_p(mass_out.data_ptr()), mass_out.shape[2],
-                                         C.c_void_p(kept.data_ptr()), C.c_void_p(new_lens.data_ptr()),
-                                         _stream_ptr(stream)), "cache_evict_paged")
+    _check(load().bgtq_cache_evict_paged(layout.handle, B_, h_kv, src.pool.data_ptr(),
+                                         src.num_pages(layout, h_kv), src.table.data_ptr(), src.max_pages,
+                                         seq_lens.data_ptr(), max_seq_len, mass.data_ptr(),
+                                         mass.shape[2], keep, n_sink, n_recent, dst.pool.data_ptr(),
+                                         dst.num_pages(layout, h_kv), dst.table.data_ptr(), dst.max_pages,
+                                         mass_out.data_ptr(), mass_out.shape[2],
+                                         kept.data_ptr(), new_lens.data_ptr(),
+                                         _raw_stream(stream)), "cache_evict_paged")
