@@ -45,7 +45,6 @@ cudaError_t launch_decode_mass(const DevLayout& L, const DecodePlan& plan, const
   m.seq_lens = seq_lens;
   m.cache = cache;
   m.most = std::min<long long>(cache.n_tiles, plan.max_tiles) * kTile;
-  m.spans = int((m.logits_ld + kMassSpan - 1) / kMassSpan);
   return launch_attention<true>(L, plan, batch, h_q, h_kv, 1, cache, seq_lens, out, workspace, 0, false, stream, nullptr, 0,
                           nullptr, nullptr, out_dtype, m);
 }

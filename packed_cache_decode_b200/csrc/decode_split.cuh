@@ -1034,12 +1034,15 @@ constexpr int kCombThreads = 512;
 // at query token gc % n_q, written to out[b][token][head]. G: columns per unit tile.
 //
 // With an attention mass to keep (mass.mass set), the CTAs past the first n_comb add the
-// cached tokens' weights to it: one CTA per (batch row, KV head, span of kMassSpan tokens)
-// forms every column's log-sum-exp from the unit's partials (M, 1 / l), then
-// mass[t] = decay mass[t] + sum over the columns of exp2(s_t - M) / l, the base-2 logits s
-// as the split kernel left them. fp32 throughout. Bound by memory (L2 where the logits fit):
-// 4 bytes per column and token read, 8 per token for the sum; recomputing the logits from
-// the codes instead would repeat the key half of the split kernel, which is bound by issue.
+// cached tokens' weights to it (or, where there are more of them than SMs, a kernel of its own
+// between the two: the merge's registers leave room for one CTA per SM, which reads the logits
+// at 1.5 TB/s; the kernel alone with five reads them at 5): one CTA per (batch row, KV head,
+// span of 4 tokens per thread) forms every column's log-sum-exp from the unit's partials
+// (M, 1 / l), then mass[t] = decay mass[t] + sum over the columns of exp2(s_t - M) / l, the
+// base-2 logits s as the split kernel left them. fp32 throughout. Bound by memory (L2 where
+// the logits fit): 4 bytes per column and token read, 8 per token for the sum; recomputing the
+// logits from the codes instead would repeat the key half of the split kernel, which is bound
+// by issue.
 struct MassArgs {
   float* mass;          // [units][ld], or null
   long long ld;
@@ -1049,11 +1052,12 @@ struct MassArgs {
   const int* seq_lens;
   CacheRef cache;       // a paged tile without a page has no logits: its tokens weigh nothing
   long long most;       // tokens a row may have
-  int n_comb;           // CTAs of the merge
+  int n_comb;           // CTAs of the merge (0: the kernel of its own)
   int spans;            // spans per unit
 };
-constexpr int kMassSpan = 4 * kCombThreads;
+constexpr int kMassThreads = 256;
 
+template <int NT>
 __device__ __forceinline__ void mass_span(const MassArgs& a, const float* part_ml, int S, int max_tiles,
                                           long long total_tiles, int n_ctas, int G, int h_q, int h_kv) {
   __shared__ float s_m[kMaxCols], s_inv[kMaxCols];
@@ -1062,10 +1066,10 @@ __device__ __forceinline__ void mass_span(const MassArgs& a, const float* part_m
   const int Gt = h_q / h_kv, CT = (Gt + kMaxG - 1) / kMaxG;
   long long len = a.seq_lens[unit / h_kv];
   len = len < 0 ? 0 : min(len, a.most);
-  const long long t0 = (long long)span * kMassSpan;
+  const long long t0 = (long long)span * (4 * NT);
   if (t0 >= len) return;
   const long long M = max_tiles;
-  for (int gc = warp; gc < Gt; gc += kCombThreads / 32) {
+  for (int gc = warp; gc < Gt; gc += NT / 32) {
     const int u = unit * CT + gc / kMaxG;
     const int n = cta_of_tile((long long)(u + 1) * M - 1, total_tiles, n_ctas) - cta_of_tile((long long)u * M, total_tiles, n_ctas) + 1;
     const float2* ml = reinterpret_cast<const float2*>(part_ml) + (size_t)u * S * G + gc % kMaxG;
@@ -1112,6 +1116,14 @@ __device__ __forceinline__ void mass_span(const MassArgs& a, const float* part_m
   }
 }
 
+__global__ void __launch_bounds__(kMassThreads) mass_kernel(const float* __restrict__ part_ml, int S, int max_tiles,
+                                                            long long total_tiles, int n_ctas, int G, int h_q, int h_kv,
+                                                            MassArgs mass) {
+  pdl_trigger();
+  pdl_wait();  // logits and partials come from split_kernel
+  mass_span<kMassThreads>(mass, part_ml, S, max_tiles, total_tiles, n_ctas, G, h_q, h_kv);
+}
+
 __device__ __forceinline__ void store_out(void* out, int dtype, size_t i, float x) {
   if (dtype == BGTQ_F32) static_cast<float*>(out)[i] = x;
   else if (dtype == BGTQ_BF16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(x);
@@ -1127,7 +1139,7 @@ __global__ void __launch_bounds__(kCombThreads, 1) combine_kernel(const float* _
   pdl_trigger();  // the next call's first kernel may start its prologue now
   if (mass.mass && int(blockIdx.x) >= mass.n_comb) {
     pdl_wait();  // logits and partials come from split_kernel
-    mass_span(mass, part_ml, S, max_tiles, total_tiles, n_ctas, G, h_q, h_kv);
+    mass_span<kCombThreads>(mass, part_ml, S, max_tiles, total_tiles, n_ctas, G, h_q, h_kv);
     return;
   }
   // column hq of row b: KV head h = hq / Gt, column gc = hq % Gt of the head, in column tile
@@ -1638,8 +1650,23 @@ cudaError_t launch_attention(const DevLayout& L, const DecodePlan& plan, int bat
     }
   });
   if (sc || e != cudaSuccess) return e;  // scores only: no merge
-  mass.n_comb = batch * hc;
-  const long long spans = mass.mass ? (long long)batch * h_kv * mass.spans : 0;
+  long long spans = 0;
+  if (mass.mass) {
+    auto spans_of = [&](int threads) { return int((mass.logits_ld + 4 * threads - 1) / (4 * threads)); };
+    mass.spans = spans_of(kCombThreads);
+    mass.n_comb = batch * hc;
+    spans = (long long)batch * h_kv * mass.spans;
+    if (spans > plan.n_ctas) {
+      mass.spans = spans_of(kMassThreads);
+      mass.n_comb = 0;
+      e = launch_dependent(mass_kernel, unsigned((long long)batch * h_kv * mass.spans), kMassThreads, stream,
+                           (const float*)a.part_ml, plan.n_parts, plan.max_tiles, a.total_tiles, plan.n_ctas, G, hc, h_kv,
+                           mass);
+      if (e != cudaSuccess) return e;
+      mass = MassArgs{};
+      spans = 0;
+    }
+  }
   return launch_dependent(combine_kernel, unsigned(batch * hc + spans), kCombThreads, stream, (const float*)a.part_ml,
                           (const float*)a.part_o, plan.n_parts, plan.max_tiles, a.total_tiles, plan.n_ctas, G, hc,
                           h_kv, n_q, L.v_rot32, out, out_dtype, rec, mass, tree);
