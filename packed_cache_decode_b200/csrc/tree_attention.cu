@@ -24,18 +24,18 @@
 // made by the preparation kernel tells. 20 warps:
 //  * warp 17: bulk copies of packed tiles into a ring;
 //  * warps 18-19: the tile's norms: scaled hi + lo pairs for the keys, fp32 for the values;
-//  * warps 8-15: decode codes into K hi, K lo and V operands in shared memory (two
-//    buffers). A quad of a lane's code string is exactly one 16-byte row of a K-major core
+//  * warps 8-15: decode codes into K hi, K lo and V operands in shared memory, two groups
+//    that take tiles in turn (one buffer each). A quad of a lane's code string is exactly one 16-byte row of a K-major core
 //    matrix (8 tokens x 8 dims), so every store of a warp is 128 consecutive bytes;
 //  * warp 16: issues the matrix instructions, Q' and P from tensor memory, K and V from
-//    shared memory: QK of tile i + 1, then PV of tile i;
+//    shared memory: QK of tile i + 2, then PV of tile i;
 //  * warps 0-7: softmax, one thread per column, two groups that take tiles in turn: S from tensor memory, P back to it. The
 //    columns' reference sits 2^5 above the maximum it was set by and moves only when a tile
 //    exceeds it by 2^3 (fp16 holds P while |v| / sqrt(128) stays below 8000), so O is seldom
 //    rescaled; the sums are right either way.
 // Q' lives in tensor memory because an M = 128, N = 64 product reading both operands from
 // shared memory would need 192 bytes per cycle of it, above the 128 there are.
-// Tensor memory columns: Q' hi and lo (up to 160), S 2 x 64, P 2 x 32, O 128.
+// Tensor memory columns: Q' hi and lo (up to 160), S 3 x 64 (each P over its own S), O 128.
 // Bound by the tensor pipe and shared memory together: per tile and 128 columns 3 x 9 + 8
 // instructions of 32-64 cycles each (1100), against some 1250 cycles of shared memory.
 //
@@ -60,7 +60,9 @@ static_assert(32 * (kNormWarp0 + 2) == kTreeThreads && kDecGroup == 4, "warps; a
 constexpr int kMaxStages = 4;
 constexpr int kMetas = 8;                 // tiles between the norm warps and the softmax: stages + 2 at most
 constexpr int kMaxDims = 160;             // packed dims as quads: kMaxQuads x 8
-constexpr int kTmemS = 160, kTmemP = 288, kTmemO = 352;
+constexpr int kSBufs = 3;                  // score tiles in tensor memory (P takes the place of its own)
+constexpr int kTmemS = 160, kTmemO = kTmemS + 64 * kSBufs;
+static_assert(kTmemO + kD <= 512, "tensor memory columns");
 constexpr unsigned kTreeWaitRounds = 1u << 12, kTreeSuspend = 10000u;  // rounds of 256 tries, nanoseconds of a try
 // key norms of a tile as the decode warps use them: per group and slot pair (tokens g + 16 p
 // and g + 16 p + 8) the rows' (hi, hi, lo, lo) fp16 of both slots, 128 consecutive bytes
@@ -193,7 +195,7 @@ __device__ __forceinline__ long long tree_row_len(const TreeLaunch& a, int b) {
 
 struct TreeShared {
   unsigned long long full[kMaxStages], normed[kMaxStages], empty[kMaxStages];
-  unsigned long long k_full[2], v_full[2], qk_done[2], p_full[2], pv_done[2], q_full, tables;
+  unsigned long long k_full[2], v_full[2], k_free[2], s_full[kSBufs], p_full[2], pv_done[2], q_full, o_done, tables;
   unsigned tmem;
   int abort, dec_ok[2][2];
   int range[kDecGroup][5][2];   // key quads of each decode warp, by rate
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.k_full[i], kDecGroup);
       mbar_init(&s.v_full[i], kDecGroup);
-      mbar_init(&s.qk_done[i], 1);
+      mbar_init(&s.k_free[i], 1);
       mbar_init(&s.p_full[i], kSoftWarps / 2);
       mbar_init(&s.pv_done[i], 1);
     }
@@ -380,7 +382,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
       mbar_init(&s.max_done[1][i], 1);
       mbar_init(&s.sum_done[i], 1);
     }
+    for (int i = 0; i < kSBufs; ++i) mbar_init(&s.s_full[i], 1);
     mbar_init(&s.q_full, kSoftWarps);
+    mbar_init(&s.o_done, 1);
     mbar_init(&s.tables, 1);
     s.abort = 0;
     fence_mbar_init();
@@ -509,6 +513,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
     bool go = true;
     const unsigned t8 = launder(t8a), t3 = launder(t3a), vt = launder(vta), units = launder(u_at) + 8u * lane;
     const unsigned kb = k_at + buf * 2u * k_part + lane4;
+    const unsigned vb = v_at + buf * 16384u + lane4 + unsigned(dw) * 4096u, v_off = L.vcode_off + dw * 256 * VR;
     unsigned i = 0;
     RingPos r;
 #pragma unroll 1
@@ -520,7 +525,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
         // the group's first warp waits (bounded) for all of it and says how that went
         if (dw == 0) {
           bool ok = tree_wait(s, &s.full[st], r.round & 1u) && tree_wait(s, &s.normed[st], r.round & 1u);
-          if (i > 1) ok = ok && tree_wait(s, &s.qk_done[buf], before);
+          if (i > 1) ok = ok && tree_wait(s, &s.k_free[buf], before);
           if (lane == 0) s.dec_ok[buf][0] = ok;
         }
         group_barrier(1 + buf);
@@ -577,9 +582,8 @@ auto quads = [&](auto rate) {
         }
         /*dec:v*/
         // values: warp dw takes chunk dw of the tile
-        const unsigned blk = tb + L.vcode_off + dw * 256 * VR, vb = v_at + buf * 16384u + lane4 + unsigned(dw) * 4096u;
-ValueLane<VR> vl;
-        vl.load(blk, lane);
+        ValueLane<VR> vl;
+        vl.load(tb + v_off, lane);
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
           unsigned x[4];
@@ -600,8 +604,9 @@ ValueLane<VR> vl;
     // the whole warp walks and waits, one elected lane issues
     const unsigned id_s = tc_idesc(kCols, kTile), id_o = tc_idesc(kCols, kD);
     const unsigned q_lo = unsigned(a.q_words);
+    RingPos ss;                      // score buffer of the next tile to score
     auto scores = [&](unsigned i) {  // S of tile i
-      const unsigned buf = i & 1u, d = tmem + kTmemS + 64u * buf;
+      const unsigned buf = i & 1u, d = tmem + kTmemS + 64u * ss.st;
       unsigned long long hi = tc_desc(k_at + buf * 2u * k_part, 1024u, 128u);
       unsigned long long lo = tc_desc(k_at + buf * 2u * k_part + k_part, 1024u, 128u);
       if (elect_one()) {
@@ -611,18 +616,23 @@ ValueLane<VR> vl;
           tc_mma(d, tmem + q_lo + 8u * k, hi, id_s, true);
           tc_mma(d, tmem + 8u * k, lo, id_s, true);
         }
-        tc_commit(&s.qk_done[buf]);
+        tc_commit(&s.k_free[buf]);
+        tc_commit(&s.s_full[ss.st]);
       }
+      ss.step(kSBufs);
       __syncwarp();
     };
-    auto values = [&](unsigned i, bool first) {  // O += P V of tile i
-      const unsigned buf = i & 1u, p = tmem + kTmemP + 32u * buf;
+    RingPos ps;                                  // score buffer that holds the next P
+    auto values = [&](unsigned i, bool first, bool last) {  // O += P V of tile i
+      const unsigned buf = i & 1u, p = tmem + kTmemS + 64u * ps.st;
       const unsigned long long v = tc_desc(v_at + buf * 16384u, 2048u, 128u);
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) tc_mma(tmem + kTmemO, p + 8u * k, v + 256u * k, id_o, !first || k > 0);
         tc_commit(&s.pv_done[buf]);
+        if (last) tc_commit(&s.o_done);
       }
+      ps.step(kSBufs);
       __syncwarp();
     };
     auto wait = [&](unsigned long long* bar, unsigned parity) {
@@ -630,27 +640,49 @@ ValueLane<VR> vl;
       tc_fence_after();
       return ok;
     };
+    auto ready = [&](unsigned long long* bar, unsigned parity) {
+      const bool ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+      tc_fence_after();
+      return ok;
+    };
     unsigned i = 0, seg = 0;
     bool go = true;
 #pragma unroll 1
     while (go && w.next(a)) {
+      // scores run two tiles ahead: QK of tile i + 2 takes the buffer of tile i - 1, whose PV was
+      // issued before it
       go = wait(&s.q_full, seg++ & 1u) && wait(&s.k_full[i & 1u], (i >> 1) & 1u);
       if (!go) break;
       scores(i);
+      if (w.n > 1) {
+        go = wait(&s.k_full[(i + 1) & 1u], ((i + 1) >> 1) & 1u);
+        if (!go) break;
+        scores(i + 1);
+      }
 #pragma unroll 1
       for (int t = 0; t < w.n; ++t, ++i) {
-        if (t + 1 < w.n) {
-          if (!wait(&s.k_full[(i + 1) & 1u], ((i + 1) >> 1) & 1u)) {
-            go = false;
+        // PV of this tile and the scores two tiles on, in the order in which they become possible
+        bool score = t + 2 < w.n, value = true;
+#pragma unroll 1
+        for (unsigned tries = 0; score || value; ++tries) {
+          if (value && ready(&s.p_full[i & 1u], (i >> 1) & 1u) && ready(&s.v_full[i & 1u], (i >> 1) & 1u)) {
+            values(i, t == 0, t + 1 == w.n);
+            value = false;
+          }
+          if (score && ready(&s.k_full[i & 1u], ((i + 2) >> 1) & 1u)) {
+            scores(i + 2);
+            score = false;
+          }
+          if ((tries & 255u) == 255u && *reinterpret_cast<volatile int*>(&s.abort)) break;
+          if (tries > kTreeWaitRounds * 256u) {
+            *reinterpret_cast<volatile int*>(&s.abort) = 1;
             break;
           }
-          scores(i + 1);
         }
-        if (!wait(&s.v_full[i & 1u], (i >> 1) & 1u) || !wait(&s.p_full[i & 1u], (i >> 1) & 1u)) {
+        if (score || value) {
           go = false;
           break;
         }
-        values(i, t == 0);
       }
     }
   } else {
@@ -680,6 +712,7 @@ ValueLane<VR> vl;
       if (lane == 0) mbar_arrive(&s.q_full);
     };
     unsigned i = 0, seg = 0;
+    RingPos sp;  // score buffer of tile i
     bool go = true, more = w.next(a);
     if (more) load_q(w.unit(a));
 #pragma unroll 1
@@ -695,13 +728,13 @@ ValueLane<VR> vl;
       const int n = w.n;
       long long before = tree_row_len(a, w.b) - nodes - (long long)w.lt0 * kTile;  // tokens before the nodes, from the tile on
 #pragma unroll 1
-      for (int t = 0; t < n; ++t, ++i, before -= kTile) {
+      for (int t = 0; t < n; ++t, ++i, sp.step(kSBufs), before -= kTile) {
         if ((i & 1u) != grp) continue;
-        const unsigned use = i >> 1;
-        if (!wait(&s.qk_done[grp], use & 1u)) {
+        if (!wait(&s.s_full[sp.st], sp.round & 1u)) {
           go = false;
           break;
         }
+        const unsigned sbuf = row + kTmemS + 64u * sp.st;
         /*softmax:after_qk*/
         tc_fence_after();
         const int valid = s.valid[i % kMetas];
@@ -710,7 +743,7 @@ ValueLane<VR> vl;
         // for the exponentials)
         unsigned x[32];
         auto load_half = [&](int h) {
-          tc_ld32(x, row + kTmemS + 64u * grp + 32u * h);
+          tc_ld32(x, sbuf + 32u * h);
           tc_wait_ld();
           if (masked) {
             // bit e: the column sees token e of the half
@@ -770,10 +803,6 @@ ValueLane<VR> vl;
         if (m != mn) l *= fast_exp2(m - mn);  // (m = -inf: l is 0)
         m = mn;
         const float mb = m == -INFINITY ? 0.f : m;  // a column that has seen nothing: weights of 0
-        if (use > 0 && !wait(&s.pv_done[grp], (use - 1) & 1u)) {  // P's buffer
-          go = false;
-          break;
-        }
         tc_fence_after();
         const unsigned long long nm = pack2(-mb, -mb);
         unsigned long long l2 = 0ull, l3 = 0ull;
@@ -796,7 +825,7 @@ ValueLane<VR> vl;
             p[e >> 1] = pack_h2(w0.x, w0.y);
             p[(e >> 1) + 1] = pack_h2(w1.x, w1.y);
           }
-          tc_st16(row + kTmemP + 32u * grp + 16u * h, p);
+          tc_st16(sbuf + 16u * h, p);  // (over scores that are read)
         }
         const float2 ls = unpack2(add2(l2, l3));
         l += ls.x + ls.y;
@@ -823,7 +852,9 @@ ValueLane<VR> vl;
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.sum_done[quad]);
       }
-      if (!wait(&s.pv_done[last & 1u], (last >> 1) & 1u)) break;
+      // (a barrier of its own, one phase a unit: pv_done may be two phases behind here, where a
+      // parity cannot tell)
+      if (!wait(&s.o_done, seg & 1u)) break;
       tc_fence_after();
       const long long slot = (long long)blockIdx.x + u;
       float4* po = a.part_o + (size_t)slot * 32 * kCols + c;
