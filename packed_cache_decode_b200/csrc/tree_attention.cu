@@ -197,7 +197,7 @@ struct TreeShared {
   unsigned long long full[kMaxStages], normed[kMaxStages], empty[kMaxStages];
   unsigned long long k_full[2], v_full[2], k_free[2], s_full[kSBufs], p_full[2], pv_done[2], q_full, o_done, tables;
   unsigned tmem;
-  int abort, dec_ok[2][2];
+  int abort;
   int range[kDecGroup][5][2];   // key quads of each decode warp, by rate
   int present[kMetas];
   float scale[kMetas][2];
@@ -219,9 +219,23 @@ struct RingPos {
   }
 };
 
+// Whether the phase of the given parity is over, without the suspension that a try may bring.
+__device__ __forceinline__ bool mbar_test(unsigned long long* bar, unsigned parity) {
+  unsigned ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0u;
+}
+
 // Waits (bounded) for the barrier's phase of the given parity; false once the CTA gives up.
 // The polling loop is kept short: the waiting warps share issue slots with the working ones.
 __device__ __forceinline__ bool tree_wait(TreeShared& s, unsigned long long* bar, unsigned parity) {
+  if (mbar_test(bar, parity)) return true;
   const unsigned addr = smem_addr(bar);
 #pragma unroll 1
   for (unsigned i = 0; i < kTreeWaitRounds; ++i) {
@@ -256,7 +270,6 @@ __device__ __forceinline__ bool tree_wait_patient(TreeShared& s, unsigned long l
   *reinterpret_cast<volatile int*>(&s.abort) = 1;
   return false;
 }
-__device__ __forceinline__ void group_barrier(int id) { asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(32 * kDecGroup) : "memory"); }
 
 // K operand words of one quad (rate R) from the lane's codes c, for its eight tokens: hi at
 // kh + 128 m, lo at kl + 128 m. nn: the lane's norms of the quad's group, (hi, lo) of slots 2j
@@ -349,7 +362,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(16) TreeShared s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int TB = L.tile_bytes, NS = a.stages;
+  const int TB = L.tile_bytes, NS = a.stages, SH = NS >> 1;  // (2 or 4 stages: the shift is 1 or 2)
   const int nq = L.n_kquads, steps = (nq + 1) >> 1;
   constexpr int kTbl = kTbl8Bytes + kTbl3Bytes + vtab_bytes<VR>();
   const unsigned k_part = unsigned(steps) * 2048u;   // bytes of a K part (hi or lo) of a buffer
@@ -426,27 +439,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
     if (lane == 0) {
       const unsigned long long pol = evict_first_policy();
       unsigned i = 0;
-      RingPos r;
       bool go = true;
 #pragma unroll 1
       while (go && w.next(a)) {
         const int h = w.head(a);
 #pragma unroll 1
-        for (int t = 0; t < w.n; ++t, ++i, r.step(NS)) {
-          if (r.round > 0 && !tree_wait_patient(s, &s.empty[r.st], (r.round - 1) & 1u)) {
+        for (int t = 0; t < w.n; ++t, ++i) {
+          const unsigned st = i & (NS - 1u), round = i >> SH;
+          if (round > 0 && !tree_wait_patient(s, &s.empty[st], (round - 1) & 1u)) {
             go = false;
             break;
           }
           const uint8_t* src = tile_ptr(a.cache, L, w.b, h, a.h_kv, w.lt0 + t);
           s.present[i % kMetas] = src != nullptr;
-          mbar_expect_tx(&s.full[r.st], src ? unsigned(TB) : 0u);
-          if (src) bulk_load(smem + (r_at - base) + r.st * TB, src, unsigned(TB), &s.full[r.st], pol);
+          mbar_expect_tx(&s.full[st], src ? unsigned(TB) : 0u);
+          if (src) bulk_load(smem + (r_at - base) + st * TB, src, unsigned(TB), &s.full[st], pol);
         }
       }
       // copies in flight land before the CTA ends: the last one of each stage
 #pragma unroll 1
       for (unsigned st = 0; st < unsigned(NS) && st < i; ++st) {
-        const unsigned rounds = (i - 1 - st) / NS;
+        const unsigned rounds = (i - 1 - st) >> SH;
         mbar_wait_bounded(&s.full[st], rounds & 1u);
       }
     }
@@ -458,15 +471,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
     const int ng = L.n_kgroups;
     const float vscale = rsqrtf(float(kD)) / L.kappa_v;
     unsigned i = 0;
-    RingPos r;
     bool go = true;
 #pragma unroll 1
     while (go && w.next(a)) {
       const long long len = tree_row_len(a, w.b);
 #pragma unroll 1
-      for (int t = 0; t < w.n; ++t, ++i, r.step(NS)) {
-        const unsigned st = r.st;
-        if (!__all_sync(0xffffffffu, tree_wait_patient(s, &s.full[st], r.round & 1u))) {
+      for (int t = 0; t < w.n; ++t, ++i) {
+        const unsigned st = i & (NS - 1u);
+        if (!__all_sync(0xffffffffu, tree_wait_patient(s, &s.full[st], i >> SH & 1u))) {
           go = false;
           break;
         }
@@ -507,33 +519,26 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
   } else if (warp >= kDecWarp0 && warp < kMmaWarp) {
     const unsigned c8 = unsigned(lane & 15) << 3, lane4 = unsigned(lane) << 2;
     // two groups take the tiles in turn (group = the operand buffer they fill)
-    const int dw = (warp - kDecWarp0) % kDecGroup, buf = (warp - kDecWarp0) / kDecGroup;
+    const unsigned dw = (warp - kDecWarp0) % kDecGroup, buf = (warp - kDecWarp0) / kDecGroup;
     // (a timeout of the tables raises the flag that the waits below see)
     tree_wait(s, &s.tables, 0u);
     bool go = true;
     const unsigned t8 = launder(t8a), t3 = launder(t3a), vt = launder(vta), units = launder(u_at) + 8u * lane;
     const unsigned kb = k_at + buf * 2u * k_part + lane4;
     const unsigned vb = v_at + buf * 16384u + lane4 + unsigned(dw) * 4096u, v_off = L.vcode_off + dw * 256 * VR;
-    unsigned i = 0;
-    RingPos r;
+    unsigned first = 0;  // the unit's first tile
 #pragma unroll 1
-    while (go && w.next(a)) {
+    for (; go && w.next(a); first += w.n) {
+      const unsigned end = first + w.n;
 #pragma unroll 1
-      for (int t = 0; t < w.n; ++t, ++i, r.step(NS)) {
-        if ((i & 1u) != unsigned(buf)) continue;
-        const unsigned st = r.st, before = ((i >> 1) - 1u) & 1u;
-        // the group's first warp waits (bounded) for all of it and says how that went
-        if (dw == 0) {
-          bool ok = tree_wait(s, &s.full[st], r.round & 1u) && tree_wait(s, &s.normed[st], r.round & 1u);
-          if (i > 1) ok = ok && tree_wait(s, &s.k_free[buf], before);
-          if (lane == 0) s.dec_ok[buf][0] = ok;
-        }
-        group_barrier(1 + buf);
+      for (unsigned i = first + ((first ^ buf) & 1u); i < end; i += 2) {
+        const unsigned st = i & (NS - 1u), before = ((i >> 1) - 1u) & 1u;
+        // (the norms came after the tile itself)
+        go = tree_wait(s, &s.normed[st], i >> SH & 1u);
+        if (i > 1) go = go && tree_wait(s, &s.k_free[buf], before);
         /*dec:start*/
-        if (!*reinterpret_cast<volatile int*>(&s.dec_ok[buf][0])) {
-          go = false;
-          break;
-        }
+        go = __all_sync(0xffffffffu, go);
+        if (!go) break;
         const unsigned tb = launder(r_at + st * TB), nb = launder(n_at + st * kNormBytes);
 auto quads = [&](auto rate) {
           constexpr int R = decltype(rate)::value;
@@ -570,15 +575,8 @@ auto quads = [&](auto rate) {
         if (lane == 0) mbar_arrive(&s.k_full[buf]);
         /*dec:kf*/
         if (i > 1) {
-          if (dw == 0) {
-            const bool ok = tree_wait(s, &s.pv_done[buf], before);
-            if (lane == 0) s.dec_ok[buf][1] = ok;
-          }
-          group_barrier(1 + buf);
-          if (!*reinterpret_cast<volatile int*>(&s.dec_ok[buf][1])) {
-            go = false;
-            break;
-          }
+          go = __all_sync(0xffffffffu, tree_wait(s, &s.pv_done[buf], before));
+          if (!go) break;
         }
         /*dec:v*/
         // values: warp dw takes chunk dw of the tile
@@ -641,7 +639,7 @@ auto quads = [&](auto rate) {
       return ok;
     };
     auto ready = [&](unsigned long long* bar, unsigned parity) {
-      const bool ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+      const bool ok = __all_sync(0xffffffffu, mbar_test(bar, parity));
       tc_fence_after();
       return ok;
     };
@@ -674,7 +672,7 @@ auto quads = [&](auto rate) {
             score = false;
           }
           if ((tries & 255u) == 255u && *reinterpret_cast<volatile int*>(&s.abort)) break;
-          if (tries > kTreeWaitRounds * 256u) {
+          if (tries > kTreeWaitRounds << 14) {
             *reinterpret_cast<volatile int*>(&s.abort) = 1;
             break;
           }
@@ -1261,7 +1259,7 @@ cudaError_t launch_tree(const DevLayout& L, const TreePlan& plan, const void* q,
   set_quads(L, a);
   const int limit = split_smem_limit();
   a.stages = kMaxStages;
-  while (a.stages > 2 && tree_smem_bytes(L, a.stages) > limit) --a.stages;
+  while (a.stages > 2 && tree_smem_bytes(L, a.stages) > limit) a.stages >>= 1;
   const int smem = tree_smem_bytes(L, a.stages);
   if (smem > limit) return cudaErrorInvalidValue;
   const long long heads = (long long)batch * h_kv;
