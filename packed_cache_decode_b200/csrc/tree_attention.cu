@@ -25,19 +25,26 @@
 //  * warp 17: bulk copies of packed tiles into a ring;
 //  * warps 18-19: the tile's norms: scaled hi + lo pairs for the keys, fp32 for the values;
 //  * warps 8-15: decode codes into K hi, K lo and V operands in shared memory, two groups
-//    that take tiles in turn (one buffer each). A quad of a lane's code string is exactly one 16-byte row of a K-major core
-//    matrix (8 tokens x 8 dims), so every store of a warp is 128 consecutive bytes;
+//    that take tiles in turn (one buffer each). A quad of a lane's code string is exactly one
+//    16-byte row of a K-major core matrix (8 tokens x 8 dims), so every store of a warp is 128
+//    consecutive bytes;
 //  * warp 16: issues the matrix instructions, Q' and P from tensor memory, K and V from
-//    shared memory: QK of tile i + 2, then PV of tile i;
-//  * warps 0-7: softmax, one thread per column, two groups that take tiles in turn: S from tensor memory, P back to it. The
-//    columns' reference sits 2^5 above the maximum it was set by and moves only when a tile
-//    exceeds it by 2^3 (fp16 holds P while |v| / sqrt(128) stays below 8000), so O is seldom
-//    rescaled; the sums are right either way.
+//    shared memory: PV of tile i and QK of tile i + 2, whichever has its operands first;
+//  * warps 0-7: softmax, one thread per column, two groups that take tiles in turn: S from
+//    tensor memory, P back over it. The columns' reference sits 2^5 above the maximum it was
+//    set by and moves only when a tile exceeds it by 2^3 (fp16 holds P while |v| / sqrt(128)
+//    stays below 8000), so O is seldom rescaled; the sums are right either way.
 // Q' lives in tensor memory because an M = 128, N = 64 product reading both operands from
 // shared memory would need 192 bytes per cycle of it, above the 128 there are.
 // Tensor memory columns: Q' hi and lo (up to 160), S 3 x 64 (each P over its own S), O 128.
-// Bound by the tensor pipe and shared memory together: per tile and 128 columns 3 x 9 + 8
-// instructions of 32-64 cycles each (1100), against some 1250 cycles of shared memory.
+// Bound: the tensor pipe needs 1100 cycles a tile and 128 columns (3 x 9 + 8 instructions of
+// 32-64 cycles), shared memory some 1250; a tile takes 2250. 64 nodes of 8 query heads per KV
+// head at 4 x 32K run in 587 us, where the products alone (three for the logits) would take
+// 270 at full rate. Half of the issue slots are used; what is left is the round trip of a
+// tile through the roles (scores, softmax, PV, decode into the freed buffer), each hand-over
+// 250-400 cycles under this load. Measured on that case and not kept: score and value
+// instructions from two warps 599 us, value codes in registers with keys decoded first 589,
+// in either order 620, a third decode group of its own for values 666.
 //
 // Every wait is bounded; a wait that runs out raises a flag that ends all roles, the status
 // says BGTQ_STATUS_TIMEOUT and copies and matrix instructions in flight are waited for
@@ -60,7 +67,7 @@ static_assert(32 * (kNormWarp0 + 2) == kTreeThreads && kDecGroup == 4, "warps; a
 constexpr int kMaxStages = 4;
 constexpr int kMetas = 8;                 // tiles between the norm warps and the softmax: stages + 2 at most
 constexpr int kMaxDims = 160;             // packed dims as quads: kMaxQuads x 8
-constexpr int kSBufs = 3;                  // score tiles in tensor memory (P takes the place of its own)
+constexpr int kSBufs = 3;                 // score tiles in tensor memory (P takes the place of its own)
 constexpr int kTmemS = 160, kTmemO = kTmemS + 64 * kSBufs;
 static_assert(kTmemO + kD <= 512, "tensor memory columns");
 constexpr unsigned kTreeWaitRounds = 1u << 12, kTreeSuspend = 10000u;  // rounds of 256 tries, nanoseconds of a try
@@ -195,7 +202,7 @@ __device__ __forceinline__ long long tree_row_len(const TreeLaunch& a, int b) {
 
 struct TreeShared {
   unsigned long long full[kMaxStages], normed[kMaxStages], empty[kMaxStages];
-  unsigned long long k_full[2], v_full[2], k_free[2], s_full[kSBufs], p_full[2], pv_done[2], q_full, o_done, tables;
+  unsigned long long k_full[2], v_full[2], k_free[2], s_full[kSBufs], p_full[2], pv_done[2], q_full, o_done, o_free, tables;
   unsigned tmem;
   int abort;
   int range[kDecGroup][5][2];   // key quads of each decode warp, by rate
@@ -398,6 +405,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
     for (int i = 0; i < kSBufs; ++i) mbar_init(&s.s_full[i], 1);
     mbar_init(&s.q_full, kSoftWarps);
     mbar_init(&s.o_done, 1);
+    mbar_init(&s.o_free, kSoftWarps);
     mbar_init(&s.tables, 1);
     s.abort = 0;
     fence_mbar_init();
@@ -536,11 +544,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
         // (the norms came after the tile itself)
         go = tree_wait(s, &s.normed[st], i >> SH & 1u);
         if (i > 1) go = go && tree_wait(s, &s.k_free[buf], before);
-        /*dec:start*/
         go = __all_sync(0xffffffffu, go);
         if (!go) break;
         const unsigned tb = launder(r_at + st * TB), nb = launder(n_at + st * kNormBytes);
-auto quads = [&](auto rate) {
+        auto quads = [&](auto rate) {
           constexpr int R = decltype(rate)::value;
           // a quad's code offset has the alignment of its own rate, and the loads are pure: the
           // launder() in here keeps them from being hoisted out of the branch on the rate
@@ -569,16 +576,13 @@ auto quads = [&](auto rate) {
         quads(IntC<3>{});
         quads(IntC<2>{});
         quads(IntC<1>{});
-        /*dec:k*/
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.k_full[buf]);
-        /*dec:kf*/
         if (i > 1) {
           go = __all_sync(0xffffffffu, tree_wait(s, &s.pv_done[buf], before));
           if (!go) break;
         }
-        /*dec:v*/
         // values: warp dw takes chunk dw of the tile
         ValueLane<VR> vl;
         vl.load(tb + v_off, lane);
@@ -595,7 +599,6 @@ auto quads = [&](auto rate) {
           mbar_arrive(&s.empty[st]);
           mbar_arrive(&s.v_full[buf]);
         }
-        /*dec:vf*/
       }
     }
   } else if (warp == kMmaWarp) {
@@ -659,6 +662,11 @@ auto quads = [&](auto rate) {
       }
 #pragma unroll 1
       for (int t = 0; t < w.n; ++t, ++i) {
+        // (both softmax groups have read the last unit's O)
+        if (t == 0 && seg > 1 && !wait(&s.o_free, seg & 1u)) {
+          go = false;
+          break;
+        }
         // PV of this tile and the scores two tiles on, in the order in which they become possible
         bool score = t + 2 < w.n, value = true;
 #pragma unroll 1
@@ -733,7 +741,6 @@ auto quads = [&](auto rate) {
           break;
         }
         const unsigned sbuf = row + kTmemS + 64u * sp.st;
-        /*softmax:after_qk*/
         tc_fence_after();
         const int valid = s.valid[i % kMetas];
         const bool masked = valid < kTile || before < kTile;  // the same for the whole CTA
@@ -766,7 +773,6 @@ auto quads = [&](auto rate) {
           mx = fmaxf(mx, fmaxf(max3(t1, __uint_as_float(x[30]), __uint_as_float(x[31])), t2) * s.scale[i % kMetas][h]);
         }
         mx *= qs;
-        /*softmax:after_ld*/
         if (i > 0 && !wait(&s.max_done[grp ^ 1u][quad], ((i - 1) >> 1) & 1u)) {
           go = false;
           break;
@@ -797,7 +803,6 @@ auto quads = [&](auto rate) {
             tc_st16(row + kTmemO + 16u * o, y);
           }
         }
-        /*softmax:after_max*/
         if (m != mn) l *= fast_exp2(m - mn);  // (m = -inf: l is 0)
         m = mn;
         const float mb = m == -INFINITY ? 0.f : m;  // a column that has seen nothing: weights of 0
@@ -827,12 +832,10 @@ auto quads = [&](auto rate) {
         }
         const float2 ls = unpack2(add2(l2, l3));
         l += ls.x + ls.y;
-        /*softmax:after_exp*/
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.p_full[grp]);
-        /*softmax:after_st*/
       }
       if (!go) break;
       // the unit's final reference is the last tile's; its last scores are done then, so the
@@ -868,6 +871,8 @@ auto quads = [&](auto rate) {
                                                           __uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3]));
       }
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.o_free);
       if (!grp) {
         if (!wait(&s.sum_done[quad], seg & 1u)) break;
         if (live) a.part_ml[(size_t)slot * kCols + c] = make_float2(mf, l + s.total[seg & 1u][c]);
