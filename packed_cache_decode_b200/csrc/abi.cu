@@ -838,13 +838,31 @@ bool tree_shape(int batch, int n_q, int h_q, int h_kv, long long max_seq_len) {
 }
 
 // Query columns of a KV head (node x query head) from which a tree call takes the tcgen05
-// kernel (128 columns per unit) instead of the decode kernel's 8-column tiles.
-constexpr int kTreeMinCols = 17;
-bool tree_wide(int h_q, int h_kv, int n_q) { return (h_q / h_kv) * n_q >= kTreeMinCols; }
+// kernel (128 columns per unit) instead of the decode kernel's 8-column tiles: more than two
+// of those, and more than three where the cache is long. The column tiles' time grows with
+// their number, the other kernel's hardly does but starts higher. Measured (B200, K2V2, bf16;
+// column tiles against tcgen05, us):
+//    columns   1 row x 1K    8 rows x 8K    4 rows x 32K    1 row x 128K
+//       16      24.1  21.9     78    92       104   153       94   154
+//       24      27.7  23.3    111    93       143   154      132   155
+//       32      28.8  23.2    138    93       181   154      167   154
+// (8 KV heads each: 128, 8192, 16384 and 16384 cache tiles).
+constexpr int kTreeMinCols = 17, kTreeMinColsLong = 25;
+constexpr long long kTreeLongTiles = 12288;
+bool tree_wide(int batch, int h_q, int h_kv, int n_q, long long max_seq_len) {
+  const long long tiles = (long long)batch * h_kv * ((max_seq_len + kTile - 1) / kTile);
+  return (h_q / h_kv) * n_q >= (tiles > kTreeLongTiles ? kTreeMinColsLong : kTreeMinCols);
+}
 
+// Between the two thresholds the path depends on max_seq_len: room for either, so that a
+// workspace sized for the longest cache serves shorter calls.
 size_t tree_workspace(int batch, int h_q, int h_kv, int n_q, long long max_seq_len, int sms) {
-  return tree_wide(h_q, h_kv, n_q) ? plan_tree(batch, h_q, h_kv, n_q, max_seq_len, sms).workspace_bytes
-                                   : plan_decode(batch, h_q * n_q, h_kv, max_seq_len, sms).workspace_bytes;
+  const int cols = (h_q / h_kv) * n_q;
+  size_t bytes = 0;
+  if (cols >= kTreeMinCols) bytes = plan_tree(batch, h_q, h_kv, n_q, max_seq_len, sms).workspace_bytes;
+  if (cols < kTreeMinColsLong)
+    bytes = std::max(bytes, plan_decode(batch, h_q * n_q, h_kv, max_seq_len, sms).workspace_bytes);
+  return bytes;
 }
 
 bgtq_status tree_impl(const DevLayout& D, const char* who, const void* q, int q_dtype, int batch, int n_q, int h_q,
@@ -870,7 +888,7 @@ bgtq_status tree_impl(const DevLayout& D, const char* who, const void* q, int q_
     return fail(BGTQ_ERR_WORKSPACE, w + ": workspace not 256-byte aligned");
   const TreeArgs tree{mask, n_nodes};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (tree_wide(h_q, h_kv, n_q))
+  if (tree_wide(batch, h_q, h_kv, n_q, max_seq_len))
     e = launch_tree(D, plan_tree(batch, h_q, h_kv, n_q, max_seq_len, sms), q, q_dtype, batch, h_q, h_kv, n_q, tree, c,
                     seq_lens, max_seq_len, softmax_scale, out, out_dtype, workspace, s);
   else
