@@ -908,13 +908,20 @@ template <int COLS>
 constexpr int kColLd = COLS + 4;   // row of columns in shared memory, 16-byte aligned
 template <int COLS>
 constexpr int kRotSmem = (kD * kD + kD * kColLd<COLS>) * int(sizeof(float));
+// Floats of the key rotations of all groups (only what the layout has: five blocks of the
+// preparation fit an SM then, instead of two).
+__host__ __device__ inline int rot_floats(const DevLayout& L) {
+  int n = 0;
+  for (int g = 0; g < L.n_kgroups; ++g) n += L.group_dim[g] * L.group_dim[g];
+  return n;
+}
 template <int COLS>
 __global__ void __launch_bounds__(256) tree_prep_kernel(DevLayout L, TreeLaunch a, const void* __restrict__ q, int q_dtype,
                                                         float qscale, long long* __restrict__ prefix,
                                                         unsigned* __restrict__ qt, float* __restrict__ q_scale) {
   extern __shared__ __align__(128) unsigned char smem[];
   float* s_rot = reinterpret_cast<float*>(smem);      // the groups' rotations, transposed, one after the other
-  float* s_q = s_rot + kD * kD;                       // [packed dim][column], then q' likewise
+  float* s_q = s_rot + rot_floats(L);                 // [packed dim][column], then q' likewise
   __shared__ float s_up[COLS];
   __shared__ short s_pc[kD], s_dim[kMaxDims];
   pdl_trigger();
@@ -1275,7 +1282,8 @@ cudaError_t launch_tree(const DevLayout& L, const TreePlan& plan, const void* q,
     static bool done[64] = {};
     const cudaError_t e = raise_smem_limit(tree_prep_kernel<COLS>, done);
     if (e != cudaSuccess) return e;
-    tree_prep_kernel<COLS><<<unsigned(heads * plan.col_tiles * (kCols / COLS)), 256, kRotSmem<COLS>, stream>>>(
+    tree_prep_kernel<COLS><<<unsigned(heads * plan.col_tiles * (kCols / COLS)), 256,
+                             kRotSmem<COLS> - (kD * kD - rot_floats(L)) * int(sizeof(float)), stream>>>(
         L, a, q, q_dtype, softmax_scale * kLog2e, reinterpret_cast<long long*>(ws + plan.prefix_at),
         reinterpret_cast<unsigned*>(ws + plan.q_at), reinterpret_cast<float*>(ws + plan.scale_at));
     return cudaGetLastError();
