@@ -39,10 +39,10 @@
 // Tensor memory columns: Q' hi and lo (up to 160), S 3 x 64 (each P over its own S), O 128.
 // Bound: the tensor pipe needs 1100 cycles a tile and 128 columns (3 x 9 + 8 instructions of
 // 32-64 cycles), shared memory some 1250; a tile takes 2250. 64 nodes of 8 query heads per KV
-// head at 4 x 32K run in 587 us, where the products alone (three for the logits) would take
-// 270 at full rate. Half of the issue slots are used; what is left is the round trip of a
+// head at 4 x 32K run in 572 us (the call), where the products alone (three for the logits) would
+// take 341 at full rate. Half of the issue slots are used; what is left is the round trip of a
 // tile through the roles (scores, softmax, PV, decode into the freed buffer), each hand-over
-// 250-400 cycles under this load. Measured on that case and not kept: score and value
+// 250-400 cycles under this load. Measured on that case (587 us then) and not kept: score and value
 // instructions from two warps 599 us, value codes in registers with keys decoded first 589,
 // in either order 620, a third decode group of its own for values 666.
 //
@@ -902,8 +902,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
 // rotations come into shared memory whole, their loads in flight together with the queries;
 // thread (packed dim p, half) then sums R_g[i][j] q[j] for half of them, a power of two per
 // column brings its largest entry near 2^13, and the fp16 hi and lo words go out in
-// tensor-memory order. Latency bound: 512 blocks of the 70B-shaped layer with 64 nodes.
-// COLS columns per block: 32, or 8 where 32 would leave SMs without one.
+// tensor-memory order. Latency bound: 512 blocks of the 70B-shaped layer with 64 nodes
+// take 30 us (cold).
+// COLS columns per block: 32, or 16 or 8 where more would leave SMs without one (8 rows
+// x 8 KV heads of 64 columns, the whole call: 32 columns 94.8, 16 86.2, 8 88.5 us).
 template <int COLS>
 constexpr int kColLd = COLS + 4;   // row of columns in shared memory, 16-byte aligned
 template <int COLS>
@@ -1090,7 +1092,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(DevLayout L, TreeLaun
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
   // kSlots partials at a time, their loads in flight together; the running maximum as usual
-  constexpr int kSlots = COLS == 32 ? 4 : 16;
+  constexpr int kSlots = COLS == 32 ? 4 : COLS == 16 ? 8 : 16;
 #pragma unroll 1
   for (int s0 = 0; live && s0 < n; s0 += kSlots) {
     float2 v[kSlots];
@@ -1276,7 +1278,8 @@ cudaError_t launch_tree(const DevLayout& L, const TreePlan& plan, const void* q,
   if (smem > limit) return cudaErrorInvalidValue;
   const long long heads = (long long)batch * h_kv;
   const int N = a.G * n_q;
-  const bool wide = heads * ((N + 31) / 32) >= plan.n_ctas;
+  // columns per block of the preparation and the merge: the most that give every SM a block
+  const int block_cols = heads * ((N + 31) / 32) >= plan.n_ctas ? 32 : heads * ((N + 15) / 16) >= plan.n_ctas ? 16 : 8;
   auto prep = [&](auto cols) {
     constexpr int COLS = decltype(cols)::value;
     static bool done[64] = {};
@@ -1288,7 +1291,7 @@ cudaError_t launch_tree(const DevLayout& L, const TreePlan& plan, const void* q,
         reinterpret_cast<unsigned*>(ws + plan.q_at), reinterpret_cast<float*>(ws + plan.scale_at));
     return cudaGetLastError();
   };
-  cudaError_t e = wide ? prep(IntC<32>{}) : prep(IntC<8>{});
+  cudaError_t e = block_cols == 32 ? prep(IntC<32>{}) : block_cols == 16 ? prep(IntC<16>{}) : prep(IntC<8>{});
   if (e != cudaSuccess) return e;
   const unsigned grid = unsigned(plan.n_ctas);
   auto go = [&](auto vr) {
@@ -1320,7 +1323,7 @@ cudaError_t launch_tree(const DevLayout& L, const TreePlan& plan, const void* q,
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, tree_combine_kernel<COLS>, L, a, plan.n_ctas, out, out_dtype);
   };
-  return wide ? combine(IntC<32>{}) : combine(IntC<8>{});
+  return block_cols == 32 ? combine(IntC<32>{}) : block_cols == 16 ? combine(IntC<16>{}) : combine(IntC<8>{});
 }
 
 }  // namespace bgtq
