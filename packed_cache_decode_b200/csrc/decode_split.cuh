@@ -807,6 +807,7 @@ __global__ void __launch_bounds__(32 * W, 1) split_kernel(DevLayout Lp, SplitArg
       // its last n_q cached tokens: column n (query token n % n_q) sees the tokens before
       // S.len - (n_q - 1 - n % n_q). Warp-uniform test: only rows from the first token
       // some column cannot see need the masks (n_q = 1: the end of the row).
+      unsigned unseen = 0;  // drafted tree: scores that the mask took out, bit 4 rt + j of sc[rt][j]
       if (EX && a.tree.mask) {
         // drafted tree: column n belongs to node n % n_q; node i of the row's last tokens is
         // seen where its bit is set, every token before them always
@@ -821,9 +822,14 @@ __global__ void __launch_bounds__(32 * W, 1) split_kernel(DevLayout Lp, SplitArg
               const long long i = gt0 + 16 * rt + 8 * k - (S.len - S.nodes);
               if (i < 0) continue;
               const bool in = i < S.nodes;
-              if (!in || !(w0 >> i & 1ull)) sc[rt][2 * k] = -INFINITY;
-              if (!in || !(w1 >> i & 1ull)) sc[rt][2 * k + 1] = -INFINITY;
+              if (!in || !(w0 >> i & 1ull)) unseen |= 1u << (4 * rt + 2 * k);
+              if (!in || !(w1 >> i & 1ull)) unseen |= 2u << (4 * rt + 2 * k);
             }
+#pragma unroll
+          for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (unseen >> (4 * rt + j) & 1u) sc[rt][j] = -INFINITY;
         }
       } else if (gt0 - g + 16 * NRT > S.len - (a.n_q - 1)) {
         const int c0 = NP ? 2 * (t & 1) : 2 * t;  // this lane's columns c0, c0 + 1
@@ -910,8 +916,17 @@ __global__ void __launch_bounds__(32 * W, 1) split_kernel(DevLayout Lp, SplitArg
         l0 += p0 + p2;
         l1 += p1 + p3;
         const float av0 = vnr[2 * rt] * vscale, av1 = vnr[2 * rt + 1] * vscale;
-        pb[rt][0] = movmatrix_trans(pack_h2(p0 * av0, p1 * av0));
-        pb[rt][1] = movmatrix_trans(pack_h2(p2 * av1, p3 * av1));
+        float w0 = p0 * av0, w1 = p1 * av0, w2 = p2 * av1, w3 = p3 * av1;
+        if constexpr (EX) {
+          // a node that the column does not see may have an infinite or NaN norm
+          const unsigned un = unseen >> (4 * rt);
+          if (un & 1u) w0 = 0.f;
+          if (un & 2u) w1 = 0.f;
+          if (un & 4u) w2 = 0.f;
+          if (un & 8u) w3 = 0.f;
+        }
+        pb[rt][0] = movmatrix_trans(pack_h2(w0, w1));
+        pb[rt][1] = movmatrix_trans(pack_h2(w2, w3));
       }
 #pragma unroll
       for (int rt = 0; rt < NRT; ++rt) {
@@ -1213,7 +1228,8 @@ __global__ void __launch_bounds__(kCombThreads, 1) combine_kernel(const float* _
     part[qtr][d] = o0 + o1;
   }
   __syncthreads();
-  if (tid < kD) op[tid] = l > 0.f ? ((part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid])) / l : 0.f;
+  // (drafted trees: a sum that is NaN stays so)
+  if (tid < kD) op[tid] = l > 0.f || (tree.mask && l != l) ? ((part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid])) / l : 0.f;
   const int heads = h_q / n_q, head = (hq / Gt) * (Gt / n_q) + gc / n_q, tok = gc % n_q;
   if (rec) {  // uniform over the grid
     float* r = rec + (((size_t)b * n_q + tok) * heads + head) * (kD + 2);

@@ -39,7 +39,7 @@
 // Tensor memory columns: Q' hi and lo (up to 160), S 3 x 64 (each P over its own S), O 128.
 // Bound: the tensor pipe needs 1100 cycles a tile and 128 columns (3 x 9 + 8 instructions of
 // 32-64 cycles), shared memory some 1250; a tile takes 2250. 64 nodes of 8 query heads per KV
-// head at 4 x 32K run in 572 us (the call), where the products alone (three for the logits) would
+// head at 4 x 32K run in 592 us (the call), where the products alone (three for the logits) would
 // take 341 at full rate. Half of the issue slots are used; what is left is the round trip of a
 // tile through the roles (scores, softmax, PV, decode into the freed buffer), each hand-over
 // 250-400 cycles under this load. Measured on that case (587 us then) and not kept: score and value
@@ -200,16 +200,19 @@ __device__ __forceinline__ long long tree_row_len(const TreeLaunch& a, int b) {
   return len < 0 ? 0 : min(len, a.most);
 }
 
+// p_full has a barrier per score buffer: a warp may be a tile of its group ahead of the others
+// (its next scores need PV of the tile between only), and its arrival for that tile must not
+// count for the one before.
 struct TreeShared {
   unsigned long long full[kMaxStages], normed[kMaxStages], empty[kMaxStages];
-  unsigned long long k_full[2], v_full[2], k_free[2], s_full[kSBufs], p_full[2], pv_done[2], q_full, o_done, o_free, tables;
+  unsigned long long k_full[2], v_full[2], k_free[2], s_full[kSBufs], p_full[kSBufs], pv_done[2], q_full, o_done, o_free, tables;
   unsigned tmem;
   int abort;
   int range[kDecGroup][5][2];   // key quads of each decode warp, by rate
   int present[kMetas];
   float scale[kMetas][2];
   int valid[kMetas];
-  unsigned long long max_done[2][4], sum_done[4];
+  unsigned long long max_done[2][4], sum_done[2][4];  // sums: by unit parity (the second group may be a unit ahead)
   float mref[kCols];            // the columns' reference maximum
   float total[2][kCols];        // the second group's sums at a unit's end (by unit parity)
   alignas(16) float vnorm[kMetas][kTile];   // |v| / (sqrt(128) kappa) by token (read four at a time)
@@ -393,16 +396,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
       mbar_init(&s.k_full[i], kDecGroup);
       mbar_init(&s.v_full[i], kDecGroup);
       mbar_init(&s.k_free[i], 1);
-      mbar_init(&s.p_full[i], kSoftWarps / 2);
       mbar_init(&s.pv_done[i], 1);
     }
 #pragma unroll 1
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s.max_done[0][i], 1);
       mbar_init(&s.max_done[1][i], 1);
-      mbar_init(&s.sum_done[i], 1);
+      mbar_init(&s.sum_done[0][i], 1);
+      mbar_init(&s.sum_done[1][i], 1);
     }
-    for (int i = 0; i < kSBufs; ++i) mbar_init(&s.s_full[i], 1);
+    for (int i = 0; i < kSBufs; ++i) {
+      mbar_init(&s.s_full[i], 1);
+      mbar_init(&s.p_full[i], kSoftWarps / 2);
+    }
     mbar_init(&s.q_full, kSoftWarps);
     mbar_init(&s.o_done, 1);
     mbar_init(&s.o_free, kSoftWarps);
@@ -503,9 +509,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
         };
         float top = 0.f;
 #pragma unroll 1
-        for (int g = 0; g < ng; ++g) top = fmaxf(top, fabsf(norm(g)));
+        for (int g = 0; g < ng; ++g) {
+          const float x = fabsf(norm(g));
+          if (x < INFINITY) top = fmaxf(top, x);  // (an infinite or NaN norm spoils its own token alone)
+        }
         const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-        const int ex = bits == 0u ? 127 : min(227, max(27, int(bits >> 23)));
+        const int ex = bits == 0u ? 127 : min(187, max(67, int(bits >> 23)));
         const float down = __int_as_float((254 - ex) << 23);
 #pragma unroll 1
         for (int g = 0; g < ng; ++g) {
@@ -671,7 +680,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
         bool score = t + 2 < w.n, value = true;
 #pragma unroll 1
         for (unsigned tries = 0; score || value; ++tries) {
-          if (value && ready(&s.p_full[i & 1u], (i >> 1) & 1u) && ready(&s.v_full[i & 1u], (i >> 1) & 1u)) {
+          if (value && ready(&s.p_full[ps.st], ps.round & 1u) && ready(&s.v_full[i & 1u], (i >> 1) & 1u)) {
             values(i, t == 0, t + 1 == w.n);
             value = false;
           }
@@ -746,15 +755,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
         const bool masked = valid < kTile || before < kTile;  // the same for the whole CTA
         // scores of one half of the tile, 32 tokens at a time (read twice: for the maximum and
         // for the exponentials)
+        // bit e: the column sees token e of the half
+        auto seen = [&](int h) {
+          const int b = int(max(-64LL, min(before - 32 * h, 32LL))), v = valid - 32 * h;
+          unsigned vis = b >= 32 ? ~0u : b > 0 ? ~0u >> (32 - b) | unsigned(mask << b) : b > -64 ? unsigned(mask >> -b) : 0u;
+          if (v < 32) vis &= v > 0 ? (1u << v) - 1u : 0u;
+          return vis;
+        };
         unsigned x[32];
         auto load_half = [&](int h) {
           tc_ld32(x, sbuf + 32u * h);
           tc_wait_ld();
           if (masked) {
-            // bit e: the column sees token e of the half
-            const int b = int(max(-64LL, min(before - 32 * h, 32LL))), v = valid - 32 * h;
-            unsigned vis = b >= 32 ? ~0u : b > 0 ? ~0u >> (32 - b) | unsigned(mask << b) : b > -64 ? unsigned(mask >> -b) : 0u;
-            if (v < 32) vis &= v > 0 ? (1u << v) - 1u : 0u;
+            const unsigned vis = seen(h);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (!(vis >> e & 1u)) x[e] = 0xff800000u;
@@ -828,6 +841,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
             p[e >> 1] = pack_h2(w0.x, w0.y);
             p[(e >> 1) + 1] = pack_h2(w1.x, w1.y);
           }
+          if (masked) {
+            // a weight of 0 times an infinite or NaN norm (of a node that the column does not see)
+            const unsigned vis = seen(h);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              p[e] &= (vis >> (2 * e) & 1u ? 0xffffu : 0u) | (vis >> (2 * e + 1) & 1u ? 0xffff0000u : 0u);
+          }
           tc_st16(sbuf + 16u * h, p);  // (over scores that are read)
         }
         const float2 ls = unpack2(add2(l2, l3));
@@ -835,7 +855,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s.p_full[grp]);
+        if (lane == 0) mbar_arrive(&s.p_full[sp.st]);
       }
       if (!go) break;
       // the unit's final reference is the last tile's; its last scores are done then, so the
@@ -851,7 +871,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
       if (grp) {
         s.total[seg & 1u][c] = l;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s.sum_done[quad]);
+        if (lane == 0) mbar_arrive(&s.sum_done[seg & 1u][quad]);
       }
       // (a barrier of its own, one phase a unit: pv_done may be two phases behind here, where a
       // parity cannot tell)
@@ -874,7 +894,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.o_free);
       if (!grp) {
-        if (!wait(&s.sum_done[quad], seg & 1u)) break;
+        if (!wait(&s.sum_done[seg & 1u][quad], (seg >> 1) & 1u)) break;
         if (live) a.part_ml[(size_t)slot * kCols + c] = make_float2(mf, l + s.total[seg & 1u][c]);
       }
       ++seg;
@@ -1028,7 +1048,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(DevLayout L, TreeLaunch 
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if ((tid & 7) == 0) {
-      const int ex = top > 0.f ? min(100, max(-100, 13 - (int(__float_as_uint(top) >> 23) - 127))) : 0;
+      const int ex = top > 0.f ? min(60, max(-60, 13 - (int(__float_as_uint(top) >> 23) - 127))) : 0;
       s_up[c] = __int_as_float((127 + ex) << 23);
       q_scale[(size_t)u * kCols + in0 + c] = __int_as_float((127 - ex) << 23);
     }
@@ -1108,7 +1128,11 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(DevLayout L, TreeLaun
     float m = top;
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) m = fmaxf(m, v[i].x);
-    if (m == -INFINITY) continue;
+    if (m == -INFINITY) {  // nothing seen (or NaN alone)
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) l += v[i].y;
+      continue;
+    }
     const float r = exp2f(top - m);
     l *= r;
 #pragma unroll
@@ -1116,7 +1140,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(DevLayout L, TreeLaun
     top = m;
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
-      if (v[i].x == -INFINITY) continue;
+      if (v[i].x == -INFINITY && v[i].y == 0.f) continue;
       const float f = exp2f(v[i].x - m);
       l = fmaf(f, v[i].y, l);
 #pragma unroll
@@ -1125,7 +1149,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(DevLayout L, TreeLaun
                            fmaf(f, x[i][j].w, o[j].w));
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
     // accumulator column n = 8 blk + g holds value dim 16 g + blk

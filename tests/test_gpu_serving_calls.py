@@ -7,15 +7,18 @@ equal bits. Two ways to the same attention output: 2e-3 relative L2 each, 4e-3 a
 of a row computed alone and in a batch: the logits are the same, the sums of up to 1000
 weights may be split elsewhere: 1000 x 2^-24 = 6e-5 of the largest weight.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
 
+import oracle as O
 from packed_cache_decode_b200 import binding as B
 
 from .parity_util import ATTN_REL_L2, rel_l2
-from .test_gpu_bounded_cache import dev, make_layouts, random_cache
-from .test_gpu_tree import random_tree, run_tree
+from .test_gpu_bounded_cache import dequantised, dev, make_layouts, random_cache
+from .test_gpu_tree import random_tree, reference, run_tree
 
 pytestmark = pytest.mark.gpu
 
@@ -46,6 +49,70 @@ def test_many_short_rows_equal_multi_token_attention():
             continue
         for x, y in zip(out[r].reshape(-1, 128), ref[r].reshape(-1, 128)):
             assert rel_l2(x, y) <= 2 * ATTN_REL_L2
+
+
+@pytest.mark.parametrize("n,h_q", [(4, 8), (24, 16)])
+def test_infinite_and_nan_norms_stay_in_their_branch(n, h_q):
+    """Two nodes with infinite and NaN norms that only they themselves see: every other node's
+    output is as if they were not there, theirs are not finite."""
+    rng = np.random.default_rng(56)
+    lay, olay = make_layouts("k2", 2)
+    h_kv, G, length = 2, h_q // 2, 200
+    tiles = random_cache(olay, 1, h_kv, 4, rng)
+    code = 64 * (olay.k_record_bytes + olay.v_record_bytes)
+    bad = (1, n - 1)
+    for i, kn, vn in ((bad[0], np.nan, np.inf), (bad[1], np.inf, np.nan)):
+        pos = length - n + i
+        entry = 8 * (pos % 8) + pos % 64 // 8
+        norms = tiles[0, :, pos // 64, code:].copy().view(np.float32).reshape(h_kv, -1, 64)
+        norms[:, :-1, entry], norms[:, -1, entry] = kn, vn
+        tiles[0, :, pos // 64, code:] = norms.reshape(h_kv, -1).view(np.uint8)
+    mask = random_tree(rng, n)
+    for j in range(n):
+        for i in bad:
+            mask[j] = (mask[j] & ~np.uint64(1 << i)) | np.uint64((1 << i) if i == j else 0)
+    q = torch.from_numpy(rng.standard_normal((1, n, h_q, 128))).to(torch.bfloat16)
+    o = run_tree(lay, q, mask[None], tiles, [length], torch.float32, False, rng).cpu().double().numpy()
+    assert lay.status() == 0
+    for h in range(h_kv):
+        ref = reference(olay, tiles[0, h], q[0, :, h * G:(h + 1) * G].double().numpy(), mask, n, length)
+        for j in range(n):
+            for a in range(G):
+                if j in bad:
+                    assert not np.isfinite(o[0, j, h * G + a]).all()
+                else:
+                    assert rel_l2(o[0, j, h * G + a], ref[j, a]) <= ATTN_REL_L2
+
+
+def test_long_rows_with_moving_maxima_are_repeatable():
+    """Rows long enough for the columns' reference maxima to move now and then, one warp at a time,
+    which lets a warp run ahead of its group: the same bits every time, and the reference's outputs."""
+    rng = np.random.default_rng(57)
+    lay, olay = make_layouts("k2", 2)
+    b, n, h_q, h_kv, length = 4, 64, 64, 8, 32768
+    tiles = random_cache(olay, b, h_kv, length // 64, rng)
+    q = torch.from_numpy(1.4 * rng.standard_normal((b, n, h_q, 128))).to(torch.bfloat16)
+    mask = np.stack([random_tree(rng, n) for _ in range(b)])
+    cache, m, lens = torch.from_numpy(tiles).cuda(), torch.from_numpy(mask.view(np.int64)).cuda(), dev([length] * b)
+    qd = q.cuda()
+    ws = torch.empty(B.tree_workspace_bytes(lay, b, h_q, h_kv, n, length), dtype=torch.uint8, device="cuda")
+    first = None
+    for _ in range(12):
+        out = torch.full((b, n, h_q, 128), float("nan"), device="cuda")
+        B.tree_attention(lay, qd, m, cache, lens, length, length, out, ws, h_kv)
+        assert torch.isfinite(out).all()
+        first = out if first is None else first
+        assert torch.equal(out, first)
+    assert lay.status() == 0
+    o, G = first.cpu().double().numpy(), h_q // h_kv
+    r, h, some = b - 1, h_kv - 1, [0, 31, 63]
+    k, v = dequantised(olay, tiles[r, h], length)
+    for j in some:
+        node = np.arange(length) - (length - n)
+        see = (node < 0) | np.array([x >= 0 and int(mask[r, j]) >> int(x) & 1 for x in node], bool)
+        ref = O.attention(q[r, j, h * G:(h + 1) * G].double().numpy(), k[see], v[see], 1 / math.sqrt(128))
+        for a in range(G):
+            assert rel_l2(o[r, j, h * G + a], ref[a]) <= ATTN_REL_L2
 
 
 def test_one_workspace_for_short_and_long_calls():
