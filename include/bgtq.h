@@ -498,7 +498,7 @@ size_t bgtq_mass_workspace_bytes(const bgtq_layout* layout, int batch, int h_q, 
  * (fp32 device, owned by the caller, zeroed before a token's first step; entries at or past
  * the length are not touched; mass_ld >= max_seq_len). decay = 1 gives the plain sum; it
  * must be finite. out [batch, h_q, 128] of out_dtype (fp32, bf16 or fp16). With a length of
- * 0 the output row is zero. Two calls at once need a workspace each. Other arguments,
+ * 0 the output row is zero; a length past max_seq_len is clipped to it and flagged. Two calls at once need a workspace each. Other arguments,
  * ownership and errors as bgtq_decode_attention. */
 bgtq_status bgtq_decode_attention_mass(const bgtq_layout* layout, const void* q, int q_dtype, int batch,
                                        int h_q, int h_kv, const void* cache, const int* seq_lens_dev,

@@ -915,8 +915,8 @@ bgtq_status mass_impl(const DevLayout& D, const char* who, const void* q, int q_
     return fail(BGTQ_ERR_WORKSPACE, w + ": workspace not 256-byte aligned");
   if (workspace_bytes < (plan.workspace_bytes + 255) / 256 * 256 + mass_logits_bytes(batch, h_q, plan))
     return fail(BGTQ_ERR_WORKSPACE, w + ": workspace smaller than bgtq_mass_workspace_bytes()");
-  cudaError_t e = launch_decode_mass(D, plan, q, q_dtype, batch, h_q, h_kv, c, seq_lens, softmax_scale, decay, mass,
-                                     mass_ld, out, out_dtype, workspace, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_decode_mass(D, plan, q, q_dtype, batch, h_q, h_kv, c, seq_lens, max_seq_len, softmax_scale,
+                                     decay, mass, mass_ld, out, out_dtype, workspace, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? BGTQ_OK : cuda_fail(e, who);
 }
 

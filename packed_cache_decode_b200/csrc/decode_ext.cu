@@ -27,9 +27,9 @@ size_t mass_logits_bytes(int batch, int h_q, const DecodePlan& plan) {
 }
 
 cudaError_t launch_decode_mass(const DevLayout& L, const DecodePlan& plan, const void* q, int q_dtype, int batch,
-                               int h_q, int h_kv, const CacheRef& cache, const int* seq_lens, float softmax_scale,
-                               float decay, float* mass, long long mass_ld, void* out, int out_dtype, void* workspace,
-                               cudaStream_t stream) {
+                               int h_q, int h_kv, const CacheRef& cache, const int* seq_lens, long long max_seq_len,
+                               float softmax_scale, float decay, float* mass, long long mass_ld, void* out,
+                               int out_dtype, void* workspace, cudaStream_t stream) {
   const int Gt = h_q / h_kv;
   const long long units = (long long)batch * h_kv * ((Gt + kMaxG - 1) / kMaxG);
   qprep_kernel<false, true><<<unsigned(units), kPrepThreads, 0, stream>>>(
@@ -44,7 +44,7 @@ cudaError_t launch_decode_mass(const DevLayout& L, const DecodePlan& plan, const
   m.logits_ld = (long long)plan.max_tiles * kTile;
   m.seq_lens = seq_lens;
   m.cache = cache;
-  m.most = std::min<long long>(cache.n_tiles, plan.max_tiles) * kTile;
+  m.most = max_seq_len;
   return launch_attention<true>(L, plan, batch, h_q, h_kv, 1, cache, seq_lens, out, workspace, 0, false, stream, nullptr, 0,
                           nullptr, nullptr, out_dtype, m);
 }

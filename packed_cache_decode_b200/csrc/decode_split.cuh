@@ -112,6 +112,7 @@ struct SplitArgs {
   int n_ctas;             // CTAs; CTA c takes tiles [c T / n_ctas, (c+1) T / n_ctas) of the sequence
   int n_parts;            // partial slots per unit
   long long total_tiles;  // units x M
+  long long most;         // tokens a row may have: longer lengths are clipped and flagged
   int h_q, h_kv, Gt;      // Gt: query columns per KV head (query heads per KV head x n_q)
   int G;                  // columns of a unit's tile: Gt when CT = 1, else 8 (the last tile may hold fewer)
   int n_q;                // query tokens per row; column n of KV head h is query token n % n_q
@@ -483,12 +484,11 @@ __device__ __forceinline__ Segment make_segment(const DevLayout& L, const SplitA
   const int b = u / a.CT / a.h_kv;
   long long len = (long long)a.seq_lens[b] + a.len_add;
   if (len < 0) len = 0;
-  const long long cap_tokens = min(a.cache.n_tiles, M) * kTile;
   const long long a0 = max(g0, (long long)u * M) - (long long)u * M;
   const long long a1 = min(g1, (long long)(u + 1) * M) - (long long)u * M;
-  if (len > cap_tokens) {
+  if (len > a.most) {
     if (flag && a0 == 0) atomicOr(L.status, BGTQ_STATUS_DECODE_CLAMPED);
-    len = cap_tokens;
+    len = a.most;
   }
   Segment s;
   if constexpr (EX) {
@@ -1066,7 +1066,7 @@ struct MassArgs {
   long long logits_ld;
   const int* seq_lens;
   CacheRef cache;       // a paged tile without a page has no logits: its tokens weigh nothing
-  long long most;       // tokens a row may have
+  long long most;       // tokens a row may have: max_seq_len
   int n_comb;           // CTAs of the merge (0: the kernel of its own)
   int spans;            // spans per unit
 };
@@ -1626,6 +1626,8 @@ cudaError_t launch_attention(const DevLayout& L, const DecodePlan& plan, int bat
   a.n_ctas = plan.n_ctas;
   a.n_parts = plan.n_parts;
   a.total_tiles = units * plan.max_tiles;
+  // (an attention mass has rows of max_seq_len entries, which may end inside a tile)
+  a.most = mass.mass ? mass.most : std::min<long long>(cache.n_tiles, plan.max_tiles) * kTile;
   a.h_q = hc;
   a.h_kv = h_kv;
   a.Gt = Gt;

@@ -90,9 +90,9 @@ cudaError_t launch_tree(const DevLayout& L, const TreePlan& plan, const void* q,
 // The workspace is the plan's (rounded up to 256 bytes) followed by mass_logits_bytes().
 size_t mass_logits_bytes(int batch, int h_q, const DecodePlan& plan);
 cudaError_t launch_decode_mass(const DevLayout& L, const DecodePlan& plan, const void* q, int q_dtype, int batch,
-                               int h_q, int h_kv, const CacheRef& cache, const int* seq_lens, float softmax_scale,
-                               float decay, float* mass, long long mass_ld, void* out, int out_dtype, void* workspace,
-                               cudaStream_t stream);
+                               int h_q, int h_kv, const CacheRef& cache, const int* seq_lens, long long max_seq_len,
+                               float softmax_scale, float decay, float* mass, long long mass_ld, void* out,
+                               int out_dtype, void* workspace, cudaStream_t stream);
 
 // The accepted path of each row's drafted tree, moved to the end of the prefix (token
 // L - n + path[i] to L - n + i), and the rows' new lengths.

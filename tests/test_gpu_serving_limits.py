@@ -1,0 +1,52 @@
+"""Lengths above max_seq_len in the calls whose buffers are sized by it: clipped to it (not to
+the end of its tile), flagged, and nothing written past the rows.
+
+The clipped call and the call with lengths that fit run the same kernels on the same tokens:
+equal bits.
+"""
+import numpy as np
+import pytest
+import torch
+
+from packed_cache_decode_b200 import binding as B
+
+from .test_gpu_bounded_cache import dev, make_layouts, paged, random_cache
+
+pytestmark = pytest.mark.gpu
+
+GUARD = 1024   # entries behind a buffer; more than the 63 of a tile that a length may exceed the limit by
+
+
+def guarded(shape, value):
+    """A contiguous tensor filled with `value` and the guard entries behind it."""
+    n = int(np.prod(shape))
+    flat = torch.full((n + GUARD,), float(value), device="cuda")
+    return flat[:n].view(*shape), flat[n:]
+
+
+@pytest.mark.parametrize("use_pages", [False, True])
+@pytest.mark.parametrize("b,h_kv,most", [(3, 2, 100), (1, 1, 1), (40, 8, 1000)])
+def test_mass_of_longer_rows_is_clipped(b, h_kv, most, use_pages):
+    """(40 rows of 1000: the sums' own kernel; else inside the merge.)"""
+    rng = np.random.default_rng(61)
+    lay, olay = make_layouts("k2", 2)
+    nt, h_q = -(-most // 64), 4 * h_kv
+    tiles = random_cache(olay, b, h_kv, nt, rng)
+    cache = paged(tiles, rng) if use_pages else torch.from_numpy(tiles).cuda()
+    q = torch.from_numpy(rng.standard_normal((b, h_q, 128))).to(torch.bfloat16).cuda()
+    ws = torch.empty(B.mass_workspace_bytes(lay, b, h_q, h_kv, most), dtype=torch.uint8, device="cuda")
+    longer = [nt * 64 - r % (nt * 64 - most) for r in range(b)]          # most + 1 .. the tile's end
+    res = []
+    for lens, status in (([most] * b, 0), (longer, B.STATUS_DECODE_CLAMPED)):
+        mass, guard = guarded((b, h_kv, most), 0.25)
+        out = torch.empty(b, h_q, 128, device="cuda")
+        if use_pages:
+            B.decode_attention_mass_paged(lay, q, cache, dev(lens), most, mass, out, ws, h_kv)
+        else:
+            B.decode_attention_mass(lay, q, cache, dev(lens), nt * 64, most, mass, out, ws, h_kv)
+        assert lay.status() == status
+        assert (guard == 0.25).all()
+        res.append((mass, out))
+    assert torch.equal(res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
+    total = res[1][0].sum(-1).cpu()      # each of the 4 query heads hands out a weight of 1
+    assert torch.allclose(total, torch.full_like(total, 4 + 0.25 * most), rtol=1e-4)
