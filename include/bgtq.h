@@ -209,7 +209,7 @@ size_t bgtq_workspace_bytes(const bgtq_layout* layout, int batch, int h_q, int h
  * (dtype as above, device; query head i uses KV head i / (h_q/h_kv)), cache as written by
  * bgtq_encode_append, seq_lens_dev[batch] int32 device = number of cached tokens of each
  * row (0 gives a zero output row), max_seq_len >= every seq_len (plans the split-K grid;
- * larger lengths are clamped and flagged), softmax_scale (e.g. 1/sqrt(128)).
+ * lengths past the last tile of 64 tokens that it reaches are clamped and flagged), softmax_scale (e.g. 1/sqrt(128)).
  * out [batch, h_q, 128] fp32 device. workspace: device buffer of at least
  * bgtq_workspace_bytes(...). h_q/h_kv must be 1..32; a KV head's query heads are taken 8 at
  * a time (each group of 8 reads the head's cache once). */
@@ -444,8 +444,8 @@ size_t bgtq_tree_workspace_bytes(const bgtq_layout* layout, int batch, int h_q, 
  * h_q, 128] of out_dtype (fp32, bf16 or fp16): rows j >= n are not written; a query that
  * sees no token gives zeros. An infinite or NaN norm of a node does not reach the queries that
  * do not see it. A row with n outside 0..n_q or above its length is flagged
- * (BGTQ_STATUS_BAD_TREE) and gets zeros. A length past max_seq_len or the capacity is
- * clamped and flagged; the nodes are then the last n tokens of the clamped row. The mask,
+ * (BGTQ_STATUS_BAD_TREE) and gets zeros. A length past max_seq_len is clamped to it and
+ * flagged; the nodes are then the last n tokens of the clamped row. The mask,
  * the lengths and the node counts are device memory; a mask of a causal run (bits 0..j of
  * node j) gives bgtq_decode_attention_multi's result. Accuracy as bgtq_decode_attention.
  * Other arguments, ownership and errors as bgtq_decode_attention; the cache must be

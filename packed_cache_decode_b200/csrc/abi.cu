@@ -893,7 +893,7 @@ bgtq_status tree_impl(const DevLayout& D, const char* who, const void* q, int q_
                     seq_lens, max_seq_len, softmax_scale, out, out_dtype, workspace, s);
   else
     e = launch_tree_columns(D, plan_decode(batch, h_q * n_q, h_kv, max_seq_len, sms), q, q_dtype, batch, h_q, h_kv, n_q,
-                            tree, c, seq_lens, softmax_scale, out, out_dtype, workspace, s);
+                            tree, c, seq_lens, max_seq_len, softmax_scale, out, out_dtype, workspace, s);
   return e == cudaSuccess ? BGTQ_OK : cuda_fail(e, who);
 }
 

@@ -10,8 +10,8 @@ namespace bgtq {
 
 cudaError_t launch_tree_columns(const DevLayout& L, const DecodePlan& plan, const void* q, int q_dtype, int batch,
                                 int h_q, int h_kv, int n_q, const TreeArgs& tree, const CacheRef& cache,
-                                const int* seq_lens, float softmax_scale, void* out, int out_dtype, void* workspace,
-                                cudaStream_t stream) {
+                                const int* seq_lens, long long max_seq_len, float softmax_scale, void* out,
+                                int out_dtype, void* workspace, cudaStream_t stream) {
   const int Gt = h_q * n_q / h_kv;
   const long long units = (long long)batch * h_kv * ((Gt + kMaxG - 1) / kMaxG);
   qprep_kernel<false, true><<<unsigned(units), kPrepThreads, 0, stream>>>(
@@ -19,7 +19,7 @@ cudaError_t launch_tree_columns(const DevLayout& L, const DecodePlan& plan, cons
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_attention<true>(L, plan, batch, h_q, h_kv, n_q, cache, seq_lens, out, workspace, 0, false, stream, nullptr, 0,
-                          nullptr, nullptr, out_dtype, MassArgs{}, tree);
+                          nullptr, nullptr, out_dtype, MassArgs{}, tree, max_seq_len);
 }
 
 size_t mass_logits_bytes(int batch, int h_q, const DecodePlan& plan) {
@@ -46,7 +46,7 @@ cudaError_t launch_decode_mass(const DevLayout& L, const DecodePlan& plan, const
   m.cache = cache;
   m.most = max_seq_len;
   return launch_attention<true>(L, plan, batch, h_q, h_kv, 1, cache, seq_lens, out, workspace, 0, false, stream, nullptr, 0,
-                          nullptr, nullptr, out_dtype, m);
+                          nullptr, nullptr, out_dtype, m, TreeArgs{}, max_seq_len);
 }
 
 }  // namespace bgtq

@@ -1598,13 +1598,15 @@ int split_warps(int v_rate, int tile_bytes, int limit) {
 // The split kernel of one call (and, unless scores only, the merge in its last CTA per
 // unit), launched as a programmatic dependent of the kernel that wrote the q' fragments
 // (and, after an append, the new tokens). n_q query tokens per row: h_q n_q query columns,
-// G = h_q n_q / h_kv per KV head.
+// G = h_q n_q / h_kv per KV head. most: tokens a row may have (-1: all tiles of the plan, the
+// rule of plain attention, whose buffers do not depend on it).
 template <bool EX>
 cudaError_t launch_attention(const DevLayout& L, const DecodePlan& plan, int batch, int h_q, int h_kv, int n_q,
                              const CacheRef& cache, const int* seq_lens, void* out, void* workspace,
                              int len_add, bool after_append, cudaStream_t stream, float* scores = nullptr,
                              long long scores_ld = 0, float* rec = nullptr, const DevLayout* heads = nullptr,
-                             int out_dtype = BGTQ_F32, MassArgs mass = MassArgs{}, TreeArgs tree = TreeArgs{}) {
+                             int out_dtype = BGTQ_F32, MassArgs mass = MassArgs{}, TreeArgs tree = TreeArgs{},
+                             long long most = -1) {
   const int hc = h_q * n_q, Gt = hc / h_kv, CT = (Gt + kMaxG - 1) / kMaxG, G = CT == 1 ? Gt : kMaxG;
   // G <= 4: the q' hi and lo parts share one m16n8k8 product (columns 0-3 and 4-7)
   const bool np = G <= 4;
@@ -1626,8 +1628,7 @@ cudaError_t launch_attention(const DevLayout& L, const DecodePlan& plan, int bat
   a.n_ctas = plan.n_ctas;
   a.n_parts = plan.n_parts;
   a.total_tiles = units * plan.max_tiles;
-  // (an attention mass has rows of max_seq_len entries, which may end inside a tile)
-  a.most = mass.mass ? mass.most : std::min<long long>(cache.n_tiles, plan.max_tiles) * kTile;
+  a.most = most >= 0 ? most : std::min<long long>(cache.n_tiles, plan.max_tiles) * kTile;
   a.h_q = hc;
   a.h_kv = h_kv;
   a.Gt = Gt;

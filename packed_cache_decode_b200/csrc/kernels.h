@@ -69,8 +69,8 @@ struct TreeArgs {
 // KV head's cache once.
 cudaError_t launch_tree_columns(const DevLayout& L, const DecodePlan& plan, const void* q, int q_dtype, int batch,
                                 int h_q, int h_kv, int n_q, const TreeArgs& tree, const CacheRef& cache,
-                                const int* seq_lens, float softmax_scale, void* out, int out_dtype, void* workspace,
-                                cudaStream_t stream);
+                                const int* seq_lens, long long max_seq_len, float softmax_scale, void* out,
+                                int out_dtype, void* workspace, cudaStream_t stream);
 
 // The same for many query columns: 128 columns per unit on tcgen05 (tree_attention.cu).
 // Workspace: offsets of its parts and its size.

@@ -10,7 +10,9 @@ import torch
 
 from packed_cache_decode_b200 import binding as B
 
+from .parity_util import ATTN_REL_L2, rel_l2
 from .test_gpu_bounded_cache import dev, make_layouts, paged, random_cache
+from .test_gpu_tree import random_tree, reference, run_tree
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +52,27 @@ def test_mass_of_longer_rows_is_clipped(b, h_kv, most, use_pages):
     assert torch.equal(res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
     total = res[1][0].sum(-1).cpu()      # each of the 4 query heads hands out a weight of 1
     assert torch.allclose(total, torch.full_like(total, 4 + 0.25 * most), rtol=1e-4)
+
+
+@pytest.mark.parametrize("use_pages", [False, True])
+@pytest.mark.parametrize("n,h_q", [(3, 2), (16, 2), (40, 8)])
+def test_tree_of_longer_rows_is_clipped(n, h_q, use_pages):
+    """A limit inside a tile, both kernels: the nodes are the last ones before the limit."""
+    rng = np.random.default_rng(62)
+    lay, olay = make_layouts("k2", 2)
+    most = 250
+    tiles = random_cache(olay, 1, 2, 5, rng)
+    q = torch.from_numpy(rng.standard_normal((1, n, h_q, 128))).to(torch.bfloat16)
+    mask = random_tree(rng, n)[None]
+    a = run_tree(lay, q, mask, tiles, [most], torch.float32, use_pages, rng, most=most)
+    assert lay.status() == 0
+    for length in (most + 1, 253, 256, 257, 300):
+        b = run_tree(lay, q, mask, tiles, [length], torch.float32, use_pages, rng, most=most)
+        assert lay.status() == B.STATUS_DECODE_CLAMPED
+        assert torch.equal(a, b)
+    G = h_q // 2
+    for h in range(2):
+        ref = reference(olay, tiles[0, h], q[0, :, h * G:(h + 1) * G].double().numpy(), mask[0], n, most)
+        for j in range(n):
+            for c in range(G):
+                assert rel_l2(a[0, j, h * G + c].cpu().double().numpy(), ref[j, c]) <= ATTN_REL_L2
