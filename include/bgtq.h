@@ -236,7 +236,7 @@ bgtq_status bgtq_decode_step(const bgtq_layout* layout, const void* k_new, const
  * softmax_scale * q_i . k_hat_t for every cached token t < seq_lens_dev[b] (k_hat decoded
  * from the packed codes: sum over groups of |k_g|/sqrt(d_g) R_g^T c[codes]), fp32 device
  * memory owned by the caller; entries at t >= seq_lens_dev[b] are not written.
- * scores_ld >= max_seq_len. Other arguments and the workspace as for
+ * scores_ld >= max_seq_len; a length past max_seq_len is clamped to it and flagged. Other arguments and the workspace as for
  * bgtq_decode_attention. Computed with the same key path as the attention (for
  * diagnostics such as the logit error of a rate allocation). */
 bgtq_status bgtq_decode_scores(const bgtq_layout* layout, const void* q, int q_dtype, int batch,

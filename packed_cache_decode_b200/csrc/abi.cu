@@ -553,8 +553,8 @@ bgtq_status scores_impl(const DevLayout& D, const char* who, const void* q, int 
   if (!workspace || workspace_bytes < plan.workspace_bytes)
     return fail(BGTQ_ERR_WORKSPACE, w + ": workspace missing or smaller than bgtq_workspace_bytes()");
   const CacheRef c{static_cast<uint8_t*>(const_cast<void*>(cache)), nullptr, capacity / kTile, 0};
-  e = launch_scores(D, plan, q, q_dtype, batch, h_q, h_kv, c, seq_lens_dev, softmax_scale, scores, scores_ld,
-                    workspace, static_cast<cudaStream_t>(stream), heads);
+  e = launch_scores(D, plan, q, q_dtype, batch, h_q, h_kv, c, seq_lens_dev, max_seq_len, softmax_scale, scores,
+                    scores_ld, workspace, static_cast<cudaStream_t>(stream), heads);
   if (e != cudaSuccess) return cuda_fail(e, who);
   return BGTQ_OK;
 }

@@ -86,8 +86,9 @@ cudaError_t launch_merge_records(const DevLayout& L, const float* recs, int n_re
 }
 
 cudaError_t launch_scores(const DevLayout& L, const DecodePlan& plan, const void* q, int q_dtype, int batch, int h_q,
-                          int h_kv, const CacheRef& cache, const int* seq_lens, float softmax_scale, float* scores,
-                          long long scores_ld, void* workspace, cudaStream_t stream, const DevLayout* heads) {
+                          int h_kv, const CacheRef& cache, const int* seq_lens, long long max_seq_len,
+                          float softmax_scale, float* scores, long long scores_ld, void* workspace,
+                          cudaStream_t stream, const DevLayout* heads) {
   const int Gt = h_q / h_kv;
   const long long units = (long long)batch * h_kv * ((Gt + kMaxG - 1) / kMaxG);
   if (heads)
@@ -99,7 +100,7 @@ cudaError_t launch_scores(const DevLayout& L, const DecodePlan& plan, const void
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_attention<false>(L, plan, batch, h_q, h_kv, 1, cache, seq_lens, nullptr, workspace, 0, false, stream,
-                          scores, scores_ld, nullptr, heads);
+                          scores, scores_ld, nullptr, heads, BGTQ_F32, MassArgs{}, TreeArgs{}, max_seq_len);
 }
 
 cudaError_t launch_decode_step(const DevLayout& L, const DecodePlan& plan, const void* k_new, const void* v_new,

@@ -55,8 +55,9 @@ cudaError_t launch_decode_step(const DevLayout& L, const DecodePlan& plan, const
 // cached token t < seq_lens[b] (the q-preparation kernel, then the split kernel in its
 // scores-only form).
 cudaError_t launch_scores(const DevLayout& L, const DecodePlan& plan, const void* q, int q_dtype, int batch, int h_q,
-                          int h_kv, const CacheRef& cache, const int* seq_lens, float softmax_scale, float* scores,
-                          long long scores_ld, void* workspace, cudaStream_t stream, const DevLayout* heads = nullptr);
+                          int h_kv, const CacheRef& cache, const int* seq_lens, long long max_seq_len,
+                          float softmax_scale, float* scores, long long scores_ld, void* workspace,
+                          cudaStream_t stream, const DevLayout* heads = nullptr);
 
 // Drafted trees of a call: mask [batch][n_q] words (bit i of node j: it sees node i),
 // n_nodes [batch] (null: n_q nodes in every row).

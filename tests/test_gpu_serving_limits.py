@@ -76,3 +76,27 @@ def test_tree_of_longer_rows_is_clipped(n, h_q, use_pages):
         for j in range(n):
             for c in range(G):
                 assert rel_l2(a[0, j, h * G + c].cpu().double().numpy(), ref[j, c]) <= ATTN_REL_L2
+
+
+@pytest.mark.parametrize("per_head", [False, True])
+@pytest.mark.parametrize("b,h_kv,h_q,most", [(3, 2, 8, 100), (1, 1, 12, 1), (2, 4, 64, 1000)])
+def test_scores_of_longer_rows_are_clipped(b, h_kv, h_q, most, per_head):
+    rng = np.random.default_rng(63)
+    lay, olay = make_layouts("k2", 2)
+    nt = -(-most // 64)
+    cache = torch.from_numpy(random_cache(olay, b, h_kv, nt, rng)).cuda()
+    q = torch.from_numpy(rng.standard_normal((b, h_q, 128))).to(torch.bfloat16).cuda()
+    ws = torch.empty(B.workspace_bytes(lay, b, h_q, h_kv, most), dtype=torch.uint8, device="cuda")
+    owner = B.LayoutSet([lay] * h_kv) if per_head else lay
+    longer = [nt * 64 - r for r in range(b)]                             # most + 1 .. the tile's end
+    res = []
+    for lens, status in (([most] * b, 0), (longer, B.STATUS_DECODE_CLAMPED)):
+        scores, guard = guarded((b, h_q, most), 0.25)
+        if per_head:
+            B.decode_scores_heads(owner, q, cache, dev(lens), nt * 64, most, scores, ws)
+        else:
+            B.decode_scores(lay, q, cache, dev(lens), nt * 64, most, scores, ws, h_kv)
+        assert owner.status() == status
+        assert (guard == 0.25).all()
+        res.append(scores)
+    assert torch.equal(*res)
