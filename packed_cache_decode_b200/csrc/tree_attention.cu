@@ -15,9 +15,12 @@
 // product to 2^-21. Powers of two keep both clear of fp16's range: one per query column, one
 // per 32 tokens (2^e, the largest norm among them); they come back as one factor of the
 // logits. The norms are folded into K because they differ per group: kept apart, every
-// group would need an accumulator of its own. P is fp16 (half a step: 2^-11 of a weight) and
-// V the fp16 value codebook (exact for rates 1-2), as in the decode kernel: folding |v| into
-// V instead would round twice.
+// group would need an accumulator of its own. P is fp16 and V the fp16 value codebook (exact
+// for rates 1-2), as in the decode kernel: folding |v| into V instead would round twice. The
+// columns' reference follows the largest entry of P itself (the weight with its value norm)
+// and puts it at 2^5.9 to 2^15.9, so an entry keeps its half step of 2^-11 down to 2^-19 of the
+// largest and is lost (while l, in fp32, counts it) below 2^-30: a token that takes nearly all
+// of the weight leaves the tail its bits, whatever its value norm.
 //
 // One CTA per SM takes an equal slice of the units' tiles (64 tokens) laid end to end, units
 // being (row, KV head, 128 columns); rows count by their true lengths, which a prefix sum
@@ -31,9 +34,8 @@
 //  * warp 16: issues the matrix instructions, Q' and P from tensor memory, K and V from
 //    shared memory: PV of tile i and QK of tile i + 2, whichever has its operands first;
 //  * warps 0-7: softmax, one thread per column, two groups that take tiles in turn: S from
-//    tensor memory, P back over it. The columns' reference sits 2^5 above the maximum it was
-//    set by and moves only when a tile exceeds it by 2^3 (fp16 holds P while |v| / sqrt(128)
-//    stays below 8000), so O is seldom rescaled; the sums are right either way.
+//    tensor memory, P back over it. A column's reference moves only when a tile has an entry of
+//    P 2^8 above the largest when it was set, so O is seldom rescaled.
 // Q' lives in tensor memory because an M = 128, N = 64 product reading both operands from
 // shared memory would need 192 bytes per cycle of it, above the 128 there are.
 // Tensor memory columns: Q' hi and lo (up to 160), S 3 x 64 (each P over its own S), O 128.
@@ -70,6 +72,10 @@ constexpr int kMaxDims = 160;             // packed dims as quads: kMaxQuads x 8
 constexpr int kSBufs = 3;                 // score tiles in tensor memory (P takes the place of its own)
 constexpr int kTmemS = 160, kTmemO = kTmemS + 64 * kSBufs;
 static_assert(kTmemO + kD <= 512, "tensor memory columns");
+// P's largest entry: exponent when the reference is set, and at most (fp16 ends at 2^16); the
+// reference is set by a bound at most 2^kEvenExp above it
+constexpr float kSetExp = 7.875f, kMoveExp = 15.875f;
+constexpr int kEvenExp = 2;
 constexpr unsigned kTreeWaitRounds = 1u << 12, kTreeSuspend = 10000u;  // rounds of 256 tries, nanoseconds of a try
 // key norms of a tile as the decode warps use them: per group and slot pair (tokens g + 16 p
 // and g + 16 p + 8) the rows' (hi, hi, lo, lo) fp16 of both slots, 128 consecutive bytes
@@ -216,7 +222,11 @@ struct TreeShared {
   float mref[kCols];            // the columns' reference maximum
   float total[2][kCols];        // the second group's sums at a unit's end (by unit parity)
   alignas(16) float vnorm[kMetas][kTile];   // |v| / (sqrt(128) kappa) by token (read four at a time)
+  alignas(16) float vlog[kMetas][kTile];    // its base-2 logarithm, -64 at least
+  float vtop[kMetas][2];        // the largest of a half, or infinity where the half spans more than 2^kEvenExp
 };
+constexpr int kTreeStatic = 7 * 1024;  // shared memory kept free of the dynamic part
+static_assert(sizeof(TreeShared) + 256 <= kTreeStatic, "static shared memory");
 
 // A position in the ring of stages: stage and parity of its current round.
 struct RingPos {
@@ -524,9 +534,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
           const unsigned at = dst + unsigned(g * kTile) * 8u + unsigned((tok >> 4) * 128 + (tok & 7) * 16 + (tok >> 3 & 1) * 8);
           asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hb | hb << 16), "r"(lb | lb << 16) : "memory");
         }
-        s.vnorm[i % kMetas][tok] = norm(ng) * vscale;
+        const float vn = norm(ng) * vscale;
+        s.vnorm[i % kMetas][tok] = vn;
+        // (at least -64: a token of no value still bounds its weight, 2^79 at most in the sum; an
+        // infinite or NaN norm leaves the reference finite)
+        auto log_of = [](float x) { return fminf(127.f, fmaxf(-64.f, __log2f(x))); };
+        s.vlog[i % kMetas][tok] = log_of(fabsf(vn));
+        const unsigned va = __float_as_uint(fabsf(vn));  // (as ordered as the norms; NaN above infinity)
+        const unsigned vmax = __reduce_max_sync(0xffffffffu, va), vmin = __reduce_min_sync(0xffffffffu, tok < valid ? va : vmax);
+        const float top_v = __uint_as_float(vmax);
+        const bool even = top_v <= __uint_as_float(vmin) * float(1 << kEvenExp) && top_v < INFINITY;
         if (lane == 0) {
           s.scale[i % kMetas][half] = __int_as_float(ex << 23);
+          s.vtop[i % kMetas][half] = even ? log_of(top_v) : INFINITY;
           if (half == 0) s.valid[i % kMetas] = valid;
         }
         __syncwarp();
@@ -773,29 +793,51 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
               if (!(vis >> e & 1u)) x[e] = 0xff800000u;
           }
         };
+        // exponent of the tile's largest entry of P, but for the reference: exact, or where the
+        // value norms of a half are within 2^kEvenExp of each other a bound at most that far above.
+        // (70B-shaped layer with 64 nodes, calls in a loop: 686 us; a reference that may rise by 2^5
+        // only 695, and exact everywhere 714; the maximum of the weights alone, which loses the
+        // tail's bits, 670.)
         float mx = -INFINITY;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           load_half(h);
-          float t1 = __uint_as_float(x[0]), t2 = __uint_as_float(x[1]);
+          const float f = s.scale[i % kMetas][h] * qs, vt = s.vtop[i % kMetas][h];
+          float t1, t2;
+          if (vt < INFINITY) {  // the same for the whole CTA
+            t1 = __uint_as_float(x[0]), t2 = __uint_as_float(x[1]);
 #pragma unroll
-          for (int e = 2; e < 30; e += 4) {
-            t1 = max3(t1, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-            t2 = max3(t2, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+            for (int e = 2; e < 30; e += 4) {
+              t1 = max3(t1, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+              t2 = max3(t2, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+            }
+            t1 = fmaf(fmaxf(max3(t1, __uint_as_float(x[30]), __uint_as_float(x[31])), t2), f, vt);
+            t2 = t1;
+          } else {
+            const unsigned long long ff = pack2(f, f);
+            const float4* vl = reinterpret_cast<const float4*>(&s.vlog[i % kMetas][32 * h]);
+            t1 = t2 = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 v = vl[e >> 2];
+              const float2 a0 = unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), ff, pack2(v.x, v.y)));
+              const float2 a1 = unpack2(fma2(pack2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), ff, pack2(v.z, v.w)));
+              t1 = max3(t1, a0.x, a0.y);
+              t2 = max3(t2, a1.x, a1.y);
+            }
           }
-          mx = fmaxf(mx, fmaxf(max3(t1, __uint_as_float(x[30]), __uint_as_float(x[31])), t2) * s.scale[i % kMetas][h]);
+          mx = max3(mx, t1, t2);
         }
-        mx *= qs;
         if (i > 0 && !wait(&s.max_done[grp ^ 1u][quad], ((i - 1) >> 1) & 1u)) {
           go = false;
           break;
         }
-        // the reference starts 2^5 above the first tile's maximum and moves when some column's
-        // tile exceeds it by 2^3, to 2^5 above that
+        // the reference starts where the first tile's largest entry is 2^kSetExp and moves, to the
+        // same place, when some column's tile has one above 2^kMoveExp
         const float mo = t > 0 ? s.mref[c] : -INFINITY;
-        const bool above = mx > mo + 3.f;
+        const bool above = mx > mo + kMoveExp;
         const bool move = __any_sync(0xffffffffu, above) || t == 0;
-        const float mn = above ? mx + 5.f : mo;
+        const float mn = above ? mx - kSetExp : mo;
         if (move) s.mref[c] = mn;
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.max_done[grp][quad]);
@@ -1295,7 +1337,7 @@ cudaError_t launch_tree(const DevLayout& L, const TreePlan& plan, const void* q,
   a.row_units = h_kv * plan.col_tiles;
   a.q_words = tree_q_words(L);
   set_quads(L, a);
-  const int limit = split_smem_limit();
+  const int limit = split_smem_limit() + kStaticReserve - kTreeStatic;
   a.stages = kMaxStages;
   while (a.stages > 2 && tree_smem_bytes(L, a.stages) > limit) a.stages >>= 1;
   const int smem = tree_smem_bytes(L, a.stages);
