@@ -442,8 +442,8 @@ size_t bgtq_tree_workspace_bytes(const bgtq_layout* layout, int batch, int h_q, 
  * or past n are ignored). n = n_nodes_dev[b], or n_q for every row when n_nodes_dev is
  * null; 1 <= n_q <= BGTQ_MAX_TREE. q [batch, n_q, h_q, 128] (q_dtype), out [batch, n_q,
  * h_q, 128] of out_dtype (fp32, bf16 or fp16): rows j >= n are not written; a query that
- * sees no token gives zeros. An infinite or NaN norm of a node does not reach the queries that
- * do not see it. A row with n outside 0..n_q or above its length is flagged
+ * sees no token gives zeros. A node's norms, however large, infinite or NaN, do not reach the
+ * queries that do not see it. A row with n outside 0..n_q or above its length is flagged
  * (BGTQ_STATUS_BAD_TREE) and gets zeros. A length past max_seq_len is clamped to it and
  * flagged; the nodes are then the last n tokens of the clamped row. The mask,
  * the lengths and the node counts are device memory; a mask of a causal run (bits 0..j of

@@ -13,8 +13,10 @@
 // and S = hi hi + lo hi + hi lo (fp32 accumulation; lo lo is 2^-22). A centroid is exact in
 // fp16 (rates 3-4: hi + lo), so hi = fp16(c n) and lo = fma(c, n_hi, -hi) + c n_lo is the
 // product to 2^-21. Powers of two keep both clear of fp16's range: one per query column, one
-// per 32 tokens (2^e, the largest norm among them); they come back as one factor of the
-// logits. The norms are folded into K because they differ per group: kept apart, every
+// per 32 tokens, which puts the largest norm among them at 2^11 (a token keeps 2^-20 of its
+// logits down to 2^-15 of that norm); they come back as one factor of the logits. In tiles with
+// drafted nodes every token has its own, so that a node's norm takes no bits from the logits of
+// queries that do not see it. The norms are folded into K because they differ per group: kept apart, every
 // group would need an accumulator of its own. P is fp16 and V the fp16 value codebook (exact
 // for rates 1-2), as in the decode kernel: folding |v| into V instead would round twice. The
 // columns' reference follows the largest entry of P itself (the weight with its value norm)
@@ -76,6 +78,7 @@ static_assert(kTmemO + kD <= 512, "tensor memory columns");
 // reference is set by a bound at most 2^kEvenExp above it
 constexpr float kSetExp = 7.875f, kMoveExp = 15.875f;
 constexpr int kEvenExp = 2;
+constexpr int kNormExp = 11;   // exponent of the largest scaled key norm (times a centroid, below 3, fp16 holds it)
 constexpr unsigned kTreeWaitRounds = 1u << 12, kTreeSuspend = 10000u;  // rounds of 256 tries, nanoseconds of a try
 // key norms of a tile as the decode warps use them: per group and slot pair (tokens g + 16 p
 // and g + 16 p + 8) the rows' (hi, hi, lo, lo) fp16 of both slots, 128 consecutive bytes
@@ -216,14 +219,16 @@ struct TreeShared {
   int abort;
   int range[kDecGroup][5][2];   // key quads of each decode warp, by rate
   int present[kMetas];
-  float scale[kMetas][2];
+  // for each half of a tile: what its key norms were divided by (1 where tokens have scales of their
+  // own), the logarithm of its largest value norm (infinity where they span more than 2^kEvenExp)
+  alignas(16) float half[kMetas][4];
   int valid[kMetas];
   unsigned long long max_done[2][4], sum_done[2][4];  // sums: by unit parity (the second group may be a unit ahead)
   float mref[kCols];            // the columns' reference maximum
   float total[2][kCols];        // the second group's sums at a unit's end (by unit parity)
   alignas(16) float vnorm[kMetas][kTile];   // |v| / (sqrt(128) kappa) by token (read four at a time)
   alignas(16) float vlog[kMetas][kTile];    // its base-2 logarithm, -64 at least
-  float vtop[kMetas][2];        // the largest of a half, or infinity where the half spans more than 2^kEvenExp
+  alignas(4) unsigned char kexp[kMetas][kTile];  // the tokens' key scales as exponent fields (tiles with drafted nodes)
 };
 constexpr int kTreeStatic = 7 * 1024;  // shared memory kept free of the dynamic part
 static_assert(sizeof(TreeShared) + 256 <= kTreeStatic, "static shared memory");
@@ -488,9 +493,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
       }
     }
   } else if (warp >= kNormWarp0) {
-    // token 32 half + lane of every tile: key norms scaled by 2^-e (e: the exponent of the
-    // largest of the 32 tokens' norms) as fp16 hi + lo, value norms over sqrt(128) kappa
-    // for the softmax
+    // token 32 half + lane of every tile: key norms scaled by 2^(kNormExp - e) (e: the exponent of
+    // the largest of the 32 tokens' norms, or of the token's own where queries may not see it) as
+    // fp16 hi + lo, value norms over sqrt(128) kappa for the softmax
     const int half = warp - kNormWarp0, tok = 32 * half + lane, entry = (tok & 7) * 8 + (tok >> 3);
     const int ng = L.n_kgroups;
     const float vscale = rsqrtf(float(kD)) / L.kappa_v;
@@ -499,6 +504,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
 #pragma unroll 1
     while (go && w.next(a)) {
       const long long len = tree_row_len(a, w.b);
+      const int full = (int(len) - (a.tree.n_nodes ? a.tree.n_nodes[w.b] : a.n_q)) / kTile;  // tiles without nodes
 #pragma unroll 1
       for (int t = 0; t < w.n; ++t, ++i) {
         const unsigned st = i & (NS - 1u);
@@ -523,9 +529,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
           const float x = fabsf(norm(g));
           if (x < INFINITY) top = fmaxf(top, x);  // (an infinite or NaN norm spoils its own token alone)
         }
-        const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-        const int ex = bits == 0u ? 127 : min(187, max(67, int(bits >> 23)));
+        const bool masked = valid < kTile || w.lt0 + t >= full;  // (as the softmax has it)
+        const unsigned all = __reduce_max_sync(0xffffffffu, __float_as_uint(top)), bits = masked ? __float_as_uint(top) : all;
+        const int ex = (bits == 0u ? 127 : min(187, max(67, int(bits >> 23)))) - kNormExp;
         const float down = __int_as_float((254 - ex) << 23);
+        s.kexp[i % kMetas][tok] = (unsigned char)ex;
 #pragma unroll 1
         for (int g = 0; g < ng; ++g) {
           const float x = norm(g) * down;
@@ -545,8 +553,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
         const float top_v = __uint_as_float(vmax);
         const bool even = top_v <= __uint_as_float(vmin) * float(1 << kEvenExp) && top_v < INFINITY;
         if (lane == 0) {
-          s.scale[i % kMetas][half] = __int_as_float(ex << 23);
-          s.vtop[i % kMetas][half] = even ? log_of(top_v) : INFINITY;
+          s.half[i % kMetas][2 * half] = masked ? 1.f : __int_as_float(ex << 23);
+          s.half[i % kMetas][2 * half + 1] = even ? log_of(top_v) : INFINITY;
           if (half == 0) s.valid[i % kMetas] = valid;
         }
         __syncwarp();
@@ -773,8 +781,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
         tc_fence_after();
         const int valid = s.valid[i % kMetas];
         const bool masked = valid < kTile || before < kTile;  // the same for the whole CTA
-        // scores of one half of the tile, 32 tokens at a time (read twice: for the maximum and
-        // for the exponentials)
         // bit e: the column sees token e of the half
         auto seen = [&](int h) {
           const int b = int(max(-64LL, min(before - 32 * h, 32LL))), v = valid - 32 * h;
@@ -782,27 +788,44 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
           if (v < 32) vis &= v > 0 ? (1u << v) - 1u : 0u;
           return vis;
         };
+        // a tile with nodes: the tokens' own scales and the mask go into the scores where they lie
+        // (a rolled loop here; as a branch of load_half it was in every tile's code twice: 732 us
+        // instead of 677 for the 70B-shaped layer with 64 nodes)
+        if (masked) {
+          const unsigned* ke = reinterpret_cast<const unsigned*>(s.kexp[i % kMetas]);
+#pragma unroll 1
+          for (int o = 0; o < 4; ++o) {
+            const unsigned vis = seen(o >> 1) >> (16 * (o & 1));
+            unsigned y[16];
+            tc_ld16(y, sbuf + 16u * o);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float k = __int_as_float((ke[4 * o + (e >> 2)] >> (8 * (e & 3)) & 0xffu) << 23);
+              y[e] = vis >> e & 1u ? __float_as_uint(__uint_as_float(y[e]) * k) : 0xff800000u;
+            }
+            tc_st16(sbuf + 16u * o, y);
+          }
+          tc_wait_st();
+        }
+        // scores of one half of the tile, 32 tokens at a time (read twice: for the maximum and
+        // for the exponentials)
         unsigned x[32];
         auto load_half = [&](int h) {
           tc_ld32(x, sbuf + 32u * h);
           tc_wait_ld();
-          if (masked) {
-            const unsigned vis = seen(h);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(vis >> e & 1u)) x[e] = 0xff800000u;
-          }
         };
         // exponent of the tile's largest entry of P, but for the reference: exact, or where the
         // value norms of a half are within 2^kEvenExp of each other a bound at most that far above.
-        // (70B-shaped layer with 64 nodes, calls in a loop: 686 us; a reference that may rise by 2^5
-        // only 695, and exact everywhere 714; the maximum of the weights alone, which loses the
-        // tail's bits, 670.)
+        // (70B-shaped layer with 64 nodes, calls in a loop, before the masks moved out of these
+        // loops: 686 us; a reference that may rise by 2^5 only 695, and exact everywhere 714; the
+        // maximum of the weights alone, which loses the tail's bits, 670.)
         float mx = -INFINITY;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
+          const float2 st = *reinterpret_cast<const float2*>(&s.half[i % kMetas][2 * h]);
           load_half(h);
-          const float f = s.scale[i % kMetas][h] * qs, vt = s.vtop[i % kMetas][h];
+          const float f = st.x * qs, vt = st.y;
           float t1, t2;
           if (vt < INFINITY) {  // the same for the whole CTA
             t1 = __uint_as_float(x[0]), t2 = __uint_as_float(x[1]);
@@ -866,9 +889,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
         unsigned long long l2 = 0ull, l3 = 0ull;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
+          const float f = s.half[i % kMetas][2 * h] * qs;
           load_half(h);
           unsigned p[16];
-          const float f = s.scale[i % kMetas][h] * qs;
           const unsigned long long ff = pack2(f, f);
           const float4* vn = reinterpret_cast<const float4*>(&s.vnorm[i % kMetas][32 * h]);
 #pragma unroll
