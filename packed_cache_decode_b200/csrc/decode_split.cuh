@@ -1098,7 +1098,7 @@ __device__ __forceinline__ void mass_span(const MassArgs& a, const float* part_m
     }
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) {
-      s_m[gc] = top;
+      s_m[gc] = top == -INFINITY ? 0.f : top;  // a column whose logits are all -inf: weights of 0
       s_inv[gc] = l > 0.f ? 1.f / l : 0.f;
     }
   }
