@@ -792,10 +792,30 @@ __global__ void __launch_bounds__(32 * W, 1) split_kernel(DevLayout Lp, SplitArg
       group(IntC<1>{});
       if constexpr (NP) {
         // columns 4..7 carried the lo parts of q': add them to the hi parts (lanes t, t^2)
+        bool inf = false;
+        if constexpr (EX) {
+          float sum = 0.f;
 #pragma unroll
-        for (int rt = 0; rt < NRT; ++rt)
+          for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sc[rt][j] += __shfl_xor_sync(0xffffffffu, sc[rt][j], 2);
+            for (int j = 0; j < 4; ++j) sum += sc[rt][j];
+          inf = __any_sync(0xffffffffu, !(fabsf(sum) < INFINITY));
+        }
+        if (inf) {
+          // an infinite norm gives both parts an infinity: the hi part's is the logit's
+#pragma unroll
+          for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float x = sc[rt][j], y = __shfl_xor_sync(0xffffffffu, x, 2), hi = t & 2 ? y : x;
+              sc[rt][j] = fabsf(hi) == INFINITY ? hi : x + y;
+            }
+        } else {
+#pragma unroll
+          for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sc[rt][j] += __shfl_xor_sync(0xffffffffu, sc[rt][j], 2);
+        }
       }
       if constexpr (EX) {
 #pragma unroll

@@ -18,7 +18,7 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("b,h_kv", [(3, 2), (40, 8)])      # the sums inside the merge; a kernel of their own
-@pytest.mark.parametrize("G", [8, 12])
+@pytest.mark.parametrize("G", [4, 8, 12])
 def test_columns_of_minus_infinity_weigh_nothing(G, b, h_kv):
     rng = np.random.default_rng(91)
     lay, olay = make_layouts("k4", 2)                       # one key group: a logit is a norm times one dot product
