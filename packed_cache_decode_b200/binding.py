@@ -738,13 +738,20 @@ def _opt(t):
     return None if t is None else t.data_ptr()
 
 
+def _row_ints(B_, *tensors):
+    """Per-row counts and lengths (None: left out): int32, one entry per row side by side, on the GPU."""
+    int32 = _torch().int32
+    for t in tensors:
+        assert t is None or (t.dtype == int32 and t.numel() == B_ and t.is_contiguous() and t.is_cuda)
+
+
 def _tree_shapes(q, tree_mask, n_nodes, seq_lens, out):
     torch = _torch()
     B_, n_q, h_q, d = q.shape
     assert d == HEAD_DIM and q.is_contiguous() and out.is_contiguous() and out.shape == q.shape
     assert tree_mask.dtype in (torch.int64, torch.uint64) and tuple(tree_mask.shape) == (B_, n_q)
-    assert tree_mask.is_contiguous() and seq_lens.dtype == torch.int32 and seq_lens.numel() == B_
-    assert n_nodes is None or (n_nodes.dtype == torch.int32 and n_nodes.numel() == B_)
+    assert tree_mask.is_contiguous() and q.is_cuda and out.is_cuda and tree_mask.is_cuda
+    _row_ints(B_, seq_lens, n_nodes)
     return B_, n_q, h_q
 
 
@@ -781,10 +788,8 @@ def tree_attention_paged(layout: Layout, q, tree_mask, cache: PagedCache, seq_le
 def _commit_shapes(path, n_path, n_nodes, seq_lens, new_lens):
     torch = _torch()
     B_, ld = path.shape
-    for t in (path, n_path, seq_lens, new_lens) + (() if n_nodes is None else (n_nodes,)):
-        assert t.dtype == torch.int32 and t.is_contiguous()
-    assert n_path.numel() == B_ and seq_lens.numel() == B_ and new_lens.numel() == B_
-    assert n_nodes is None or n_nodes.numel() == B_
+    assert path.dtype == torch.int32 and path.is_contiguous() and path.is_cuda
+    _row_ints(B_, n_path, seq_lens, new_lens, n_nodes)
     return B_, ld
 
 
@@ -820,11 +825,13 @@ def mass_workspace_bytes(layout: Layout, batch: int, h_q: int, h_kv: int, max_se
     return int(n)
 
 
-def _mass_shapes(q, mass, out, h_kv):
+def _mass_shapes(q, seq_lens, mass, out, h_kv):
     torch = _torch()
     B_, h_q, d = q.shape
     assert d == HEAD_DIM and q.is_contiguous() and out.is_contiguous() and out.shape == q.shape
     assert mass.dtype == torch.float32 and mass.is_contiguous() and tuple(mass.shape[:2]) == (B_, h_kv)
+    assert q.is_cuda and out.is_cuda and mass.is_cuda
+    _row_ints(B_, seq_lens)
     return B_, h_q
 
 
@@ -833,7 +840,7 @@ def decode_attention_mass(layout: Layout, q, cache, seq_lens, capacity: int, max
     """decode_attention that also adds each cached token's attention weight, summed over its
     KV head's query heads, to decay times mass [B, h_kv, >= max_seq_len] (fp32 CUDA).
     q [B, h_q, 128]; out like q (fp32, bf16 or fp16)."""
-    B_, h_q = _mass_shapes(q, mass, out, h_kv)
+    B_, h_q = _mass_shapes(q, seq_lens, mass, out, h_kv)
     scale = 1.0 / HEAD_DIM ** 0.5 if softmax_scale is None else float(softmax_scale)
     _check(load().bgtq_decode_attention_mass(layout.handle, q.data_ptr(), dtype_code(q), B_, h_q, h_kv,
                                              cache.data_ptr(), seq_lens.data_ptr(), capacity,
@@ -846,7 +853,7 @@ def decode_attention_mass(layout: Layout, q, cache, seq_lens, capacity: int, max
 def decode_attention_mass_paged(layout: Layout, q, cache: PagedCache, seq_lens, max_seq_len: int, mass, out,
                                 workspace, h_kv: int, decay: float = 1.0, softmax_scale: float | None = None,
                                 stream=None):
-    B_, h_q = _mass_shapes(q, mass, out, h_kv)
+    B_, h_q = _mass_shapes(q, seq_lens, mass, out, h_kv)
     assert cache.table.shape[0] == B_
     scale = 1.0 / HEAD_DIM ** 0.5 if softmax_scale is None else float(softmax_scale)
     _check(load().bgtq_decode_attention_mass_paged(layout.handle, q.data_ptr(), dtype_code(q), B_, h_q,
@@ -865,8 +872,8 @@ def _evict_shapes(mass, mass_out, kept, seq_lens, new_lens, keep, h_kv):
     assert mass.dtype == torch.float32 and mass.is_contiguous() and mass.shape[1] == h_kv
     assert mass_out.dtype == torch.float32 and mass_out.is_contiguous() and tuple(mass_out.shape[:2]) == (B_, h_kv)
     assert kept.dtype == torch.int32 and kept.is_contiguous() and tuple(kept.shape) == (B_, h_kv, keep)
-    for t in (seq_lens, new_lens):
-        assert t.dtype == torch.int32 and t.is_contiguous() and t.numel() == B_
+    assert mass.is_cuda and mass_out.is_cuda and kept.is_cuda
+    _row_ints(B_, seq_lens, new_lens)
     return B_
 
 
