@@ -227,11 +227,10 @@ struct TreeShared {
   float mref[kCols];            // the columns' reference maximum
   float total[2][kCols];        // the second group's sums at a unit's end (by unit parity)
   alignas(16) float vnorm[kMetas][kTile];   // |v| / (sqrt(128) kappa) by token (read four at a time)
-  alignas(16) float vlog[kMetas][kTile];    // its base-2 logarithm, -64 at least
+  alignas(16) __half vlog[kMetas][kTile];   // its base-2 logarithm, -64 at least (to 2^-5: a bound's accuracy)
   alignas(4) unsigned char kexp[kMetas][kTile];  // the tokens' key scales as exponent fields (tiles with drafted nodes)
 };
-constexpr int kTreeStatic = 7 * 1024;  // shared memory kept free of the dynamic part
-static_assert(sizeof(TreeShared) + 256 <= kTreeStatic, "static shared memory");
+static_assert(sizeof(TreeShared) + 64 <= kStaticReserve, "static shared memory");
 
 // A position in the ring of stages: stage and parity of its current round.
 struct RingPos {
@@ -547,7 +546,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
         // (at least -64: a token of no value still bounds its weight, 2^79 at most in the sum; an
         // infinite or NaN norm leaves the reference finite)
         auto log_of = [](float x) { return fminf(127.f, fmaxf(-64.f, __log2f(x))); };
-        s.vlog[i % kMetas][tok] = log_of(fabsf(vn));
+        s.vlog[i % kMetas][tok] = __float2half_rn(log_of(fabsf(vn)));
         const unsigned va = __float_as_uint(fabsf(vn));  // (as ordered as the norms; NaN above infinity)
         const unsigned vmax = __reduce_max_sync(0xffffffffu, va), vmin = __reduce_min_sync(0xffffffffu, tok < valid ? va : vmax);
         const float top_v = __uint_as_float(vmax);
@@ -838,13 +837,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
             t2 = t1;
           } else {
             const unsigned long long ff = pack2(f, f);
-            const float4* vl = reinterpret_cast<const float4*>(&s.vlog[i % kMetas][32 * h]);
+            const uint2* vl = reinterpret_cast<const uint2*>(&s.vlog[i % kMetas][32 * h]);
             t1 = t2 = -INFINITY;
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              const float4 v = vl[e >> 2];
-              const float2 a0 = unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), ff, pack2(v.x, v.y)));
-              const float2 a1 = unpack2(fma2(pack2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), ff, pack2(v.z, v.w)));
+              const uint2 v = vl[e >> 2];
+              const float2 v0 = __half22float2(as_h2(v.x)), v1 = __half22float2(as_h2(v.y));
+              const float2 a0 = unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), ff, pack2(v0.x, v0.y)));
+              const float2 a1 = unpack2(fma2(pack2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), ff, pack2(v1.x, v1.y)));
               t1 = max3(t1, a0.x, a0.y);
               t2 = max3(t2, a1.x, a1.y);
             }
@@ -1360,7 +1360,7 @@ cudaError_t launch_tree(const DevLayout& L, const TreePlan& plan, const void* q,
   a.row_units = h_kv * plan.col_tiles;
   a.q_words = tree_q_words(L);
   set_quads(L, a);
-  const int limit = split_smem_limit() + kStaticReserve - kTreeStatic;
+  const int limit = split_smem_limit();
   a.stages = kMaxStages;
   while (a.stages > 2 && tree_smem_bytes(L, a.stages) > limit) a.stages >>= 1;
   const int smem = tree_smem_bytes(L, a.stages);
