@@ -522,26 +522,28 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
           }
           return x;
         };
+        float kn[kMaxGroups];  // (all loads in flight together)
+#pragma unroll
+        for (int g = 0; g < kMaxGroups; ++g) kn[g] = g < ng ? norm(g) : 0.f;
+        const float vn = norm(ng) * vscale;
         float top = 0.f;
-#pragma unroll 1
-        for (int g = 0; g < ng; ++g) {
-          const float x = fabsf(norm(g));
-          if (x < INFINITY) top = fmaxf(top, x);  // (an infinite or NaN norm spoils its own token alone)
-        }
+#pragma unroll
+        for (int g = 0; g < kMaxGroups; ++g)
+          if (fabsf(kn[g]) < INFINITY) top = fmaxf(top, fabsf(kn[g]));  // (an infinite or NaN norm spoils its own token alone)
         const bool masked = valid < kTile || w.lt0 + t >= full;  // (as the softmax has it)
         const unsigned all = __reduce_max_sync(0xffffffffu, __float_as_uint(top)), bits = masked ? __float_as_uint(top) : all;
         const int ex = (bits == 0u ? 127 : min(187, max(67, int(bits >> 23)))) - kNormExp;
         const float down = __int_as_float((254 - ex) << 23);
         s.kexp[i % kMetas][tok] = (unsigned char)ex;
-#pragma unroll 1
-        for (int g = 0; g < ng; ++g) {
-          const float x = norm(g) * down;
+#pragma unroll
+        for (int g = 0; g < kMaxGroups; ++g) {
+          if (g >= ng) break;
+          const float x = kn[g] * down;
           const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
           const unsigned hb = __half_as_ushort(hi), lb = __half_as_ushort(lo);
           const unsigned at = dst + unsigned(g * kTile) * 8u + unsigned((tok >> 4) * 128 + (tok & 7) * 16 + (tok >> 3 & 1) * 8);
           asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hb | hb << 16), "r"(lb | lb << 16) : "memory");
         }
-        const float vn = norm(ng) * vscale;
         s.vnorm[i % kMetas][tok] = vn;
         // (at least -64: a token of no value still bounds its weight, 2^79 at most in the sum; an
         // infinite or NaN norm leaves the reference finite)
@@ -814,42 +816,42 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
           tc_ld32(x, sbuf + 32u * h);
           tc_wait_ld();
         };
-        // exponent of the tile's largest entry of P, but for the reference: exact, or where the
-        // value norms of a half are within 2^kEvenExp of each other a bound at most that far above.
-        // (70B-shaped layer with 64 nodes, calls in a loop, before the masks moved out of these
-        // loops: 686 us; a reference that may rise by 2^5 only 695, and exact everywhere 714; the
-        // maximum of the weights alone, which loses the tail's bits, 670.)
-        float mx = -INFINITY;
+        // exponent of the tile's largest entry of P, but for the reference: where the value norms of
+        // both halves are within 2^kEvenExp of each other a bound at most that far above, else
+        // exact, in a second look. (64 nodes at 4 x 32K, K2V2, 64 heads, in a CUDA graph: 602 us; the
+        // maximum of the weights alone, which loses the tail's bits, 593; both ways in one
+        // loop 605; in a loop of calls exact everywhere 714 where this takes 680. A reference
+        // that may rise by 2^5 before it moves, not 2^8, costs 10.)
+        float mx = -INFINITY, even = 0.f;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           const float2 st = *reinterpret_cast<const float2*>(&s.half[i % kMetas][2 * h]);
           load_half(h);
-          const float f = st.x * qs, vt = st.y;
-          float t1, t2;
-          if (vt < INFINITY) {  // the same for the whole CTA
-            t1 = __uint_as_float(x[0]), t2 = __uint_as_float(x[1]);
+          float t1 = __uint_as_float(x[0]), t2 = __uint_as_float(x[1]);
 #pragma unroll
-            for (int e = 2; e < 30; e += 4) {
-              t1 = max3(t1, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-              t2 = max3(t2, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
-            }
-            t1 = fmaf(fmaxf(max3(t1, __uint_as_float(x[30]), __uint_as_float(x[31])), t2), f, vt);
-            t2 = t1;
-          } else {
-            const unsigned long long ff = pack2(f, f);
-            const uint2* vl = reinterpret_cast<const uint2*>(&s.vlog[i % kMetas][32 * h]);
-            t1 = t2 = -INFINITY;
+          for (int e = 2; e < 30; e += 4) {
+            t1 = max3(t1, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+            t2 = max3(t2, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+          }
+          t1 = fmaxf(max3(t1, __uint_as_float(x[30]), __uint_as_float(x[31])), t2);
+          mx = fmaxf(mx, fmaf(t1, st.x * qs, st.y));
+          even = fmaxf(even, st.y);
+        }
+        if (!(even < INFINITY)) {  // the same for the whole CTA
+          mx = -INFINITY;
+#pragma unroll 1
+          for (int o = 0; o < 4; ++o) {
+            unsigned y[16];
+            tc_ld16(y, sbuf + 16u * o);
+            tc_wait_ld();
+            const float f = s.half[i % kMetas][o & 2] * qs;
+            const unsigned* vl = reinterpret_cast<const unsigned*>(&s.vlog[i % kMetas][16 * o]);
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const uint2 v = vl[e >> 2];
-              const float2 v0 = __half22float2(as_h2(v.x)), v1 = __half22float2(as_h2(v.y));
-              const float2 a0 = unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), ff, pack2(v0.x, v0.y)));
-              const float2 a1 = unpack2(fma2(pack2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), ff, pack2(v1.x, v1.y)));
-              t1 = max3(t1, a0.x, a0.y);
-              t2 = max3(t2, a1.x, a1.y);
+            for (int e = 0; e < 16; e += 2) {
+              const float2 v = __half22float2(as_h2(vl[e >> 1]));
+              mx = max3(mx, fmaf(__uint_as_float(y[e]), f, v.x), fmaf(__uint_as_float(y[e + 1]), f, v.y));
             }
           }
-          mx = max3(mx, t1, t2);
         }
         if (i > 0 && !wait(&s.max_done[grp ^ 1u][quad], ((i - 1) >> 1) & 1u)) {
           go = false;
