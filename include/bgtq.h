@@ -470,15 +470,17 @@ bgtq_status bgtq_tree_attention_paged(const bgtq_layout* layout, const void* q, 
  * append overwrites them; tokens from there to seq_len keep their bytes). path_dev
  * [batch, path_ld] (path_ld >= n_q), n_path_dev[batch], n as in bgtq_tree_attention
  * (n_nodes_dev or n_q); new_lens_dev[batch] receives the lengths and must not overlap
- * seq_lens_dev. A path may name nodes in any order, or one twice. A row whose n, n_path,
+ * seq_lens_dev, path_dev, n_path_dev or n_nodes_dev. A path may name nodes in any order, or one twice. A row whose n, n_path,
  * path or length does not fit (n_path > n, a node outside 0..n-1, n > seq_len, seq_len >
- * capacity) is flagged (BGTQ_STATUS_BAD_TREE) and keeps its tokens and its length. */
+ * capacity) is flagged (BGTQ_STATUS_BAD_TREE) and keeps its tokens and its length. After
+ * BGTQ_STATUS_TIMEOUT the rows' nodes and new lengths are invalid. */
 bgtq_status bgtq_tree_commit(const bgtq_layout* layout, const int* path_dev, int path_ld,
                              const int* n_path_dev, const int* n_nodes_dev, int n_q, int batch, int h_kv,
                              void* cache, const int* seq_lens_dev, int* new_lens_dev, long long capacity,
                              void* stream);
 /* The same on a paged cache (a row with a page outside the pool among its nodes' tiles is
- * flagged BGTQ_STATUS_BAD_PAGE and keeps its tokens; its new length is written). */
+ * flagged BGTQ_STATUS_BAD_PAGE and keeps its tokens; its new length is written). The pages that
+ * hold a row's nodes must not be another row's too. */
 bgtq_status bgtq_tree_commit_paged(const bgtq_layout* layout, const int* path_dev, int path_ld,
                                    const int* n_path_dev, const int* n_nodes_dev, int n_q, int batch,
                                    int h_kv, void* pool, long long num_pages, const int* block_table_dev,
@@ -523,8 +525,8 @@ bgtq_status bgtq_decode_attention_mass_paged(const bgtq_layout* layout, const vo
  * kept; the rest of a row's last tile is zeroed, later tiles are not touched. mass
  * [batch, h_kv, mass_ld >= max_seq_len]; mass_out [batch, h_kv, mass_out_ld] receives the
  * kept tokens' mass, then zeros up to mass_out_ld; kept_dev [batch, h_kv, keep] int32 their
- * old positions, then -1; new_lens_dev[batch] = min(seq_len, keep). Needs keep >= 1,
- * n_sink, n_recent >= 0, n_sink + n_recent <= keep; lengths past max_seq_len are clamped
+ * old positions, then -1; new_lens_dev[batch] = min(seq_len, keep). Needs keep >= 1, batch *
+ * h_kv <= 65535, n_sink, n_recent >= 0, n_sink + n_recent <= keep; lengths past max_seq_len are clamped
  * and flagged. No buffer that is written may overlap one that is read (checked for the
  * caches, the masses and the lengths); caches must be 16-byte aligned. */
 bgtq_status bgtq_cache_evict(const bgtq_layout* layout, int batch, int h_kv, const void* src,

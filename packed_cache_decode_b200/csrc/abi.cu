@@ -823,6 +823,11 @@ bgtq_status commit_impl(const DevLayout& D, const char* who, const int* path, in
   if (!aligned16(c.base)) return fail(BGTQ_ERR_INVALID, w + ": cache not 16-byte aligned");
   bgtq_status st = check_unaliased_lens(w, seq_lens, new_lens, batch);
   if (st != BGTQ_OK) return st;
+  // (the first KV head's CTA writes a row's new length while the others still read its path)
+  const size_t rows = size_t(batch) * 4;
+  if (overlaps(path, (size_t(batch - 1) * path_ld + n_q) * 4, new_lens, rows) || overlaps(n_path, rows, new_lens, rows) ||
+      (n_nodes && overlaps(n_nodes, rows, new_lens, rows)))
+    return fail(BGTQ_ERR_INVALID, w + ": new_lens must not overlap path, n_path or n_nodes");
   cudaError_t e = launch_commit(D, batch, h_kv, path, path_ld, n_path, n_nodes, n_q, c, seq_lens, new_lens,
                                 static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? BGTQ_OK : cuda_fail(e, who);
