@@ -844,13 +844,14 @@ bool tree_shape(int batch, int n_q, int h_q, int h_kv, long long max_seq_len) {
 
 // Query columns of a KV head (node x query head) from which a tree call takes the tcgen05
 // kernel (128 columns per unit) instead of the decode kernel's 8-column tiles: more than two
-// of those, and more than three where the cache is long. The column tiles' time grows with
-// their number, the other kernel's hardly does but starts higher. Measured (B200, K2V2, bf16;
-// column tiles against tcgen05, us):
+// of those, and more than three where the cache is long (by max_seq_len: the host does not know the
+// lengths). The column tiles' time grows with their number, the other kernel's hardly does but
+// starts higher; two tiles lose 2 us in the smallest call and win 18 to 66 in the others. Measured
+// (B200, K2V2, bf16, CUDA graph; column tiles against tcgen05, us):
 //    columns   1 row x 1K    8 rows x 8K    4 rows x 32K    1 row x 128K
-//       16      24.1  21.9     78    92       104   153       94   154
-//       24      27.7  23.3    111    93       143   154      132   155
-//       32      28.8  23.2    138    93       181   154      167   154
+//       16      24.2  22.1     78    96       104   160       95   161
+//       24      28.3  23.8    111    97       144   160      133   161
+//       32      28.8  23.8    138    97       182   161      168   161
 // (8 KV heads each: 128, 8192, 16384 and 16384 cache tiles).
 constexpr int kTreeMinCols = 17, kTreeMinColsLong = 25;
 constexpr long long kTreeLongTiles = 12288;

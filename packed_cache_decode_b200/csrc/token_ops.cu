@@ -308,8 +308,8 @@ __device__ __forceinline__ int row_tokens(const int* seq_lens, int b, long long 
 // One CTA per (row, KV head): the one or two tiles that hold the row's drafted tokens come
 // into shared memory whole before anything is written, so a path may name its nodes in any
 // order. A path that leaves every token in its place writes nothing. Latency bound: one
-// round trip to memory for the lengths and the path, one for the tiles (8 CTAs 3.5 us, 512
-// CTAs of two tiles each 6.3 us in a CUDA graph).
+// round trip to memory for the lengths and the path, one for the tiles (8 CTAs 4.1 us, 512
+// CTAs of two tiles each 6.8 us in a CUDA graph).
 __global__ void __launch_bounds__(kCommitThreads) commit_kernel(DevLayout L, const __grid_constant__ QuadList ql, CacheRef cache, const int* __restrict__ path,
                                                               int path_ld, const int* __restrict__ n_path,
                                                               const int* __restrict__ n_nodes, int n_q,

@@ -43,7 +43,8 @@
 // Tensor memory columns: Q' hi and lo (up to 160), S 3 x 64 (each P over its own S), O 128.
 // Bound: the tensor pipe needs 1100 cycles a tile and 128 columns (3 x 9 + 8 instructions of
 // 32-64 cycles), shared memory some 1250; a tile takes 2250. 64 nodes of 8 query heads per KV
-// head at 4 x 32K run in 592 us (the call), where the products alone (three for the logits) would
+// head at 4 x 32K run in 602 us (the call in a CUDA graph over one cache; 681 in a loop of
+// calls over three caches in turn), where the products alone (three for the logits) would
 // take 341 at full rate. Half of the issue slots are used; what is left is the round trip of a
 // tile through the roles (scores, softmax, PV, decode into the freed buffer), each hand-over
 // 250-400 cycles under this load. Measured on that case (587 us then) and not kept: score and value
