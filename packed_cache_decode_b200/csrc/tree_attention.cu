@@ -16,12 +16,13 @@
 // per 32 tokens, which puts the largest norm among them at 2^11 (a token keeps 2^-20 of its
 // logits down to 2^-15 of that norm); they come back as one factor of the logits. In tiles with
 // drafted nodes every token has its own, so that a node's norm takes no bits from the logits of
-// queries that do not see it. The norms are folded into K because they differ per group: kept apart, every
-// group would need an accumulator of its own. P is fp16 and V the fp16 value codebook (exact
-// for rates 1-2), as in the decode kernel: folding |v| into V instead would round twice. The
-// columns' reference follows the largest entry of P itself (the weight with its value norm)
-// and puts it at 2^5.9 to 2^15.9, so an entry keeps its half step of 2^-11 down to 2^-19 of the
-// largest and is lost (while l, in fp32, counts it) below 2^-30: a token that takes nearly all
+// queries that do not see it. The norms are folded into K because they differ per group: kept
+// apart, every group would need an accumulator of its own. P is fp16 (V as fp16 has one product
+// per tile; a hi + lo P would need two) and V the fp16 value codebook (exact for rates 1-2, to
+// 1.8e-5 and 9.3e-5 for rates 3 and 4), as in the decode kernel: folding |v| into V instead would
+// round twice. The columns' reference follows the largest entry of P itself (the weight with its value norm)
+// and puts it at 2^4.9 to 2^15.9, so an entry keeps its half step of 2^-11 down to 2^-18 of the
+// largest and is lost (while l, in fp32, counts it) below 2^-29: a token that takes nearly all
 // of the weight leaves the tail its bits, whatever its value norm.
 //
 // One CTA per SM takes an equal slice of the units' tiles (64 tokens) laid end to end, units
@@ -78,7 +79,7 @@ static_assert(kTmemO + kD <= 512, "tensor memory columns");
 // P's largest entry: exponent when the reference is set, and at most (fp16 ends at 2^16); the
 // reference is set by a bound at most 2^kEvenExp above it
 constexpr float kSetExp = 7.875f, kMoveExp = 15.875f;
-constexpr int kEvenExp = 2;
+constexpr int kEvenExp = 3;
 constexpr int kNormExp = 11;   // exponent of the largest scaled key norm (times a centroid, below 3, fp16 holds it)
 constexpr unsigned kTreeWaitRounds = 1u << 12, kTreeSuspend = 10000u;  // rounds of 256 tries, nanoseconds of a try
 // key norms of a tile as the decode warps use them: per group and slot pair (tokens g + 16 p
@@ -822,7 +823,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(DevLayout L, Tree
         // exact, in a second look. (64 nodes at 4 x 32K, K2V2, 64 heads, in a CUDA graph: 602 us; the
         // maximum of the weights alone, which loses the tail's bits, 593; both ways in one
         // loop 605; in a loop of calls exact everywhere 714 where this takes 680. A reference
-        // that may rise by 2^5 before it moves, not 2^8, costs 10.)
+        // that may rise by 2^5 before it moves, not 2^8, costs 10. Tiles that all need the second
+        // look: 7 to 12 % more.)
         float mx = -INFINITY, even = 0.f;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {

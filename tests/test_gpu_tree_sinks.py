@@ -3,8 +3,8 @@ token of small value and a long tail of values that share a direction, so that t
 tail's. Both kernels, contiguous and paged.
 
 Tolerance: the library's 2e-3 relative L2 (fp32 outputs). Weights are fp16 with their value norms.
-In the kernel for many columns an entry keeps half a step of 2^-11 down to 2^-19 of the
-largest one seen and is lost below 2^-30, so every tail here is within its reach. The kernel for few
+In the kernel for many columns an entry keeps half a step of 2^-11 down to 2^-18 of the
+largest one seen and is lost below 2^-29, so every tail here is within its reach. The kernel for few
 columns has the reference of plain decode attention, the largest weight of a warp's tokens at 1:
 where the tail's entries are fp16 subnormals next to the sink (step 2^-24) a warp's share of the
 tail loses up to 2^-25 / (2^-drop value) of itself, so its tails stop at 2^-18.
